@@ -15,6 +15,7 @@ Layouts (row-major, contiguous, on the GPU):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -24,6 +25,9 @@ from . import build as _build
 
 HISA_F32, HISA_BF16, HISA_E4M3 = 0, 1, 2
 OP_BLOCK, OP_TOKEN, OP_FLAT, OP_FLAT_SAMPLED, OP_BLOCK_REFINE, OP_FROM_HOST = 1, 2, 3, 4, 5, 6
+OP_ATTENTION_KV4 = 7
+NORMS = {"rms": 1, "layer": 2}
+KV4_WIDTH, KV4_LATENT, KV4_RECORD = 576, 512, 416   # features of a latent row, of its latent part; bytes of its 4-bit record
 STATUS = {0: "HISA_OK", 1: "HISA_ERR_INVALID_ARG", 2: "HISA_ERR_UNSUPPORTED", 3: "HISA_ERR_WORKSPACE",
           4: "HISA_ERR_CUDA", 5: "HISA_ERR_TIMEOUT"}
 
@@ -40,7 +44,7 @@ class Shape(ctypes.Structure):
                  "dtype")]
 
 
-_P = ctypes.c_void_p
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _SIGS = {
     "hisa_pool_blocks": [_P, _P, _P, _P, ctypes.POINTER(Shape), _P],
     "hisa_pool_blocks_range": [_P, _P, _P, _P, ctypes.POINTER(Shape), ctypes.c_int32, ctypes.c_int32, _P],
@@ -62,6 +66,13 @@ _SIGS = {
     "hisa_indexer_from_host": [_P, _P, _P, _P, _P, _P, ctypes.POINTER(Shape), _P, ctypes.c_int32, _P,
                                ctypes.c_size_t, _P],
     "hisa_sparse_attention": [_P, _P, _P] + [ctypes.c_int32] * 7 + [ctypes.c_float, _P, _P, _P],
+    "hisa_rotary": [_P, _I64, _I64, _P, _P, _I64] + [_I32] * 6 + [ctypes.c_float, _I32, _P, _I64, _I64, _P],
+    "hisa_norm_rotary": [_P, _I64, _I64, _P, _P, _I64] + [_I32] * 4 + [_P, _P, ctypes.c_float] + [_I32] * 3 +
+                        [ctypes.c_float, _I32, _P, _I64, _I64, _P],
+    "hisa_kv4_write": [_P, _I64, _P, _I64, _P, _I64, _P],
+    "hisa_kv4_read": [_P, _I64, _P, _I64, _P, _I64, _P],
+    "hisa_sparse_attention_kv4": [_P, _P, _I32, _I32, _P, _P] + [_I32] * 5 + [ctypes.c_float, _P, _P, _P,
+                                                                             ctypes.c_size_t, _P],
     "hisa_workspace_size": [ctypes.c_int32, ctypes.POINTER(Shape), ctypes.POINTER(ctypes.c_size_t)],
     "hisa_get_status": [_P],
     "hisa_selftest_wait_timeout": [ctypes.c_uint64, _P],
@@ -106,6 +117,11 @@ def _check(status: int, where: str):
 
 def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
+
+
+def _device_of(t: torch.Tensor):
+    """Makes t's device current (its current stream is then the one used)."""
+    return torch.cuda.device(t.device)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -394,6 +410,199 @@ def hisa_block_refine_topm(q, w, kpool, n_visible, superblock_idx, *, num_keys: 
                                          group, ctypes.byref(shape), out.data_ptr(), ws.data_ptr(), ws.numel(),
                                          _stream()), "hisa_block_refine_topm")
     return out
+
+
+def rotary_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                    original_positions: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                    amplitude_factor: float = 0.1, device="cuda"):
+    """Frequencies of hisa_rotary: (inv_freq [rotary_dim / 2] float64, amplitude).
+
+    Unscaled, pair i turns by base^(-2i / rotary_dim) radians per position.  For contexts longer than the
+    `original_positions` a model was trained on:
+      "linear"  every pair is slowed by `factor` (positions are interpolated);
+      "ntk"     the base grows by factor^(rotary_dim / (rotary_dim - 2)): the fastest pair keeps its speed, the
+                slowest is slowed by `factor`;
+      "ramp"    pairs that turn at least beta_fast times over original_positions keep their speed, those that
+                turn at most beta_slow times are slowed by `factor`, with a ramp linear in the pair's index
+                between; the amplitude is amplitude_factor * ln(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and >= 2")
+    if not (base > 1 and factor > 0):
+        raise ValueError("base must be above 1 and factor above 0")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    f, amplitude = base ** (-i / rotary_dim), 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ntk":
+        if rotary_dim > 2:
+            f = (base * factor ** (rotary_dim / (rotary_dim - 2))) ** (-i / rotary_dim)
+    elif scaling == "ramp":
+        if factor < 1 or not beta_fast > beta_slow > 0 or original_positions < 1:
+            raise ValueError("ramp needs factor >= 1, beta_fast > beta_slow > 0 and original_positions >= 1")
+
+        def index_of(turns):       # the (real) pair index that turns this often over original_positions
+            return rotary_dim * math.log(original_positions / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo = max(math.floor(index_of(beta_fast)), 0)
+        hi = min(math.ceil(index_of(beta_slow)), rotary_dim - 1)
+        slow = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * (1 - slow) + f / factor * slow
+        amplitude = amplitude_factor * math.log(factor) + 1.0
+    elif scaling is not None:
+        raise ValueError(f"unknown scaling {scaling!r}: linear, ntk or ramp")
+    return f.to(device), amplitude
+
+
+def _rows_of(x: torch.Tensor, name: str):
+    """(tokens, heads, dim, token stride, head stride) of x [tokens, heads, dim] or
+    [batch, Q, heads, dim] whose features are contiguous and whose batch and Q
+    axes are one axis in memory."""
+    if not x.is_cuda or x.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, dim] or [batch, Q, heads, dim]")
+    heads, dim = x.shape[-2:]
+    if dim < 1 or heads < 1 or (dim > 1 and x.stride(-1) != 1):
+        raise ValueError(f"{name}'s features must be contiguous")
+    tokens, ts = (x.shape[0], x.stride(0)) if x.dim() == 3 else (x.shape[0] * x.shape[1], x.stride(1))
+    if x.dim() == 4 and x.shape[0] > 1:
+        if x.shape[1] == 1:
+            ts = x.stride(0)
+        elif x.stride(0) != x.shape[1] * x.stride(1) and tokens:
+            raise ValueError(f"{name}'s batch and Q axes must be one axis in memory")
+    return tokens, heads, dim, ts, x.stride(-2)
+
+
+def _on(device, name: str, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors of {name} must be on one device, got {device} and {t.device}")
+
+
+def _rotary(name, x, positions, inv_freq, offset, out, weight=None, bias=None):
+    tokens, heads, dim, ts, hs = _rows_of(x, "x")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.shape != x.shape[:-2]:
+        raise ValueError(f"positions must be contiguous int32 {tuple(x.shape[:-2])}")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2]")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    _, _, _, ots, ohs = _rows_of(out, "out")
+    _on(x.device, name, positions, inv_freq, out, weight, bias)
+    return tokens, heads, dim, ts, hs, out, ots, ohs
+
+
+def hisa_rotary(x, positions, inv_freq, *, offset: int = 0, interleaved: bool = False, amplitude: float = 1.0,
+                reverse: bool = False, out: Optional[torch.Tensor] = None):
+    """Rotary positions: features [offset, offset + 2 * len(inv_freq)) of x
+    [tokens, heads, dim] or [batch, Q, heads, dim] (float32 / bfloat16, any token
+    and head strides) turned by positions (int32, x's leading shape).  inv_freq
+    (float64) and amplitude come from rotary_inv_freq.  out=x turns in place
+    and touches only the turned features; reverse=True turns back (the
+    gradient).  Returns out."""
+    tokens, heads, dim, ts, hs, out, ots, ohs = _rotary("hisa_rotary", x, positions, inv_freq, offset, out)
+    with _device_of(x):
+        _check(load().hisa_rotary(x.data_ptr(), ts, hs, positions.data_ptr(), inv_freq.data_ptr(), tokens, heads, dim,
+                                  2 * inv_freq.numel(), offset, int(interleaved), int(reverse), amplitude,
+                                  dtype_code(x), out.data_ptr(), ots, ohs, _stream()), "hisa_rotary")
+    return out
+
+
+def hisa_norm_rotary(x, positions, inv_freq, *, weight, bias=None, norm: str = "rms", eps: float = 1e-6,
+                     norm_dim: Optional[int] = None, offset: int = 0, interleaved: bool = False,
+                     amplitude: float = 1.0, out: Optional[torch.Tensor] = None):
+    """The RMS ("rms") or layer ("layer") norm of each head's features [0, norm_dim)
+    (default: all) with fp32 weight (and bias), then hisa_rotary's turn, in
+    one pass.  Returns out (out=x works in place)."""
+    tokens, heads, dim, ts, hs, out, ots, ohs = _rotary("hisa_norm_rotary", x, positions, inv_freq, offset, out, weight,
+                                                        bias)
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
+    norm_dim = dim if norm_dim is None else norm_dim
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (norm_dim,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous float32 [{norm_dim}]")
+    with _device_of(x):
+        _check(load().hisa_norm_rotary(x.data_ptr(), ts, hs, positions.data_ptr(), inv_freq.data_ptr(), tokens, heads,
+                                       dim, NORMS[norm], norm_dim, weight.data_ptr(), _ptr(bias), eps,
+                                       2 * inv_freq.numel(), offset, int(interleaved), amplitude, dtype_code(x),
+                                       out.data_ptr(), ots, ohs, _stream()), "hisa_norm_rotary")
+    return out
+
+
+def _check_kv4(cache: torch.Tensor):
+    _need(cache, "cache", 3)
+    if cache.dtype != torch.uint8 or cache.shape[2] != KV4_RECORD or cache.shape[0] < 1 or cache.shape[1] < 1:
+        raise ValueError(f"cache must be uint8 [num_pages, page_size, {KV4_RECORD}], got {cache.dtype} "
+                         f"{tuple(cache.shape)}")
+
+
+def _check_kv4_rows(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor):
+    if not rows.is_cuda or rows.dim() != 2 or rows.shape[1] != KV4_WIDTH or rows.dtype != torch.bfloat16 or \
+            rows.stride(1) != 1:
+        raise ValueError(f"rows must be a bfloat16 CUDA tensor [n, {KV4_WIDTH}] with contiguous features")
+    if slots.dtype != torch.int32 or tuple(slots.shape) != (rows.shape[0],) or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous int32 [n]")
+    _on(cache.device, "the 4-bit cache", rows, slots)
+    return rows.stride(0) if rows.shape[0] > 1 else KV4_WIDTH
+
+
+def hisa_kv4_write(rows, slots, cache) -> None:
+    """Quantise latent rows [n, 576] bf16 (row stride a multiple of 8) into the
+    records `slots` [n] int32 of the 4-bit cache [num_pages, page_size, 416]
+    uint8: slot = page * page_size + row of the page; slots below 0 are skipped."""
+    _check_kv4(cache)
+    stride = _check_kv4_rows(rows, slots, cache)
+    with _device_of(cache):
+        _check(load().hisa_kv4_write(rows.data_ptr(), stride, slots.data_ptr(), rows.shape[0], cache.data_ptr(),
+                                     cache.shape[0] * cache.shape[1], _stream()), "hisa_kv4_write")
+
+
+def hisa_kv4_read(cache, slots, out: Optional[torch.Tensor] = None):
+    """The latent rows [n, 576] bf16 that the records `slots` [n] int32 stand for
+    (zeros for slots below 0)."""
+    _check_kv4(cache)
+    if out is None:
+        out = torch.empty((slots.shape[0], KV4_WIDTH), dtype=torch.bfloat16, device=cache.device)
+    stride = _check_kv4_rows(out, slots, cache)
+    with _device_of(cache):
+        _check(load().hisa_kv4_read(cache.data_ptr(), cache.shape[0] * cache.shape[1], slots.data_ptr(), out.shape[0],
+                                    out.data_ptr(), stride, _stream()), "hisa_kv4_read")
+    return out
+
+
+def hisa_sparse_attention_kv4(q, cache, page_table, idx, *, scale: float, num_keys: int,
+                              workspace: Optional[torch.Tensor] = None):
+    """hisa_sparse_attention over the 4-bit paged cache: q [batch, Q, H, 576] bf16,
+    cache [num_pages, page_size, 416] uint8, page_table [batch,
+    ceil(num_keys / page_size)] int32, idx [batch, Q, top_k] int32 ->
+    (o [batch, Q, H, 512] bf16, lse [batch, Q, H] fp32)."""
+    _need(q, "q", 4)
+    _check_kv4(cache)
+    _need(page_table, "page_table", 2)
+    _need(idx, "idx", 3)
+    b, Q, H, dqk = q.shape
+    if q.dtype != torch.bfloat16 or dqk != KV4_WIDTH:
+        raise TypeError(f"q must be bfloat16 [batch, Q, H, {KV4_WIDTH}]")
+    if idx.dtype != torch.int32 or idx.shape[:2] != (b, Q):
+        raise ValueError("idx must be int32 [batch, Q, top_k]")
+    pages = -(-num_keys // cache.shape[1])
+    if page_table.dtype != torch.int32 or tuple(page_table.shape) != (b, pages):
+        raise ValueError(f"page_table must be int32 {(b, pages)}, got {page_table.dtype} {tuple(page_table.shape)}")
+    _on(q.device, "hisa_sparse_attention_kv4", cache, page_table, idx, workspace)
+    with _device_of(q):
+        o = torch.empty((b, Q, H, KV4_LATENT), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((b, Q, H), dtype=torch.float32, device=q.device)
+        need = workspace_size(OP_ATTENTION_KV4, Shape(b, num_keys, Q, H, 0, 0, 0, idx.shape[2], HISA_BF16))
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = _workspace(need, q.device)
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(load().hisa_sparse_attention_kv4(q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1],
+                                                page_table.data_ptr(), idx.data_ptr(), b, Q, num_keys, H, idx.shape[2],
+                                                float(scale), o.data_ptr(), lse.data_ptr(), _ptr(workspace), nbytes,
+                                                _stream()), "hisa_sparse_attention_kv4")
+    return o, lse
 
 
 class HisaIndexer3:

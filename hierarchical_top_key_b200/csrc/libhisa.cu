@@ -22,6 +22,9 @@
 #include "flat_lite.cuh"
 #include "sort.cuh"
 #include "sparse_attn.cuh"
+#include "rotary.cuh"
+#include "kv4.cuh"
+#include "kv4_attn.cuh"
 
 using namespace hisa;
 
@@ -321,6 +324,23 @@ hisa_status token_simt_h(const hisa_shape* s, const void* q, const float* qsc, c
   if (s->heads <= 4) return launch_token_simt<DT, 4>(s, q, qsc, w, k, ksc, nvis, bidx, oi, os, st);
   if (s->heads <= 16) return launch_token_simt<DT, 16>(s, q, qsc, w, k, ksc, nvis, bidx, oi, os, st);
   return launch_token_simt<DT, 64>(s, q, qsc, w, k, ksc, nvis, bidx, oi, os, st);
+}
+
+// ------------------------------------------------------------ 4-bit latent cache
+
+hisa_status check_kv4_attn(int32_t batch, int32_t num_queries, int32_t heads, int32_t top_k) {
+  if (batch < 1 || num_queries < 1 || heads < 1)
+    return fail(HISA_ERR_INVALID_ARG, "batch, num_queries and heads must be >= 1");
+  if (top_k < 1 || top_k > kKv4MaxK) return fail(HISA_ERR_UNSUPPORTED, "top_k must be in [1, %d]", kKv4MaxK);
+  return HISA_OK;
+}
+
+hisa_status kv4_workspace(const hisa_shape* s, size_t* bytes) {
+  if (!s) return fail(HISA_ERR_INVALID_ARG, "shape is NULL");
+  hisa_status e = check_kv4_attn(s->batch, s->num_queries, s->heads, s->top_k);
+  if (e != HISA_OK) return e;
+  *bytes = 0;
+  return HISA_OK;
 }
 
 constexpr size_t kSmemBudget = 232448;   // 227 KB opt-in dynamic shared memory per CTA
@@ -671,6 +691,7 @@ hisa_status hisa_get_status(hisa_stream stream) {
 
 hisa_status hisa_workspace_size(int32_t op, const hisa_shape* s, size_t* bytes) {
   if (!bytes) return fail(HISA_ERR_INVALID_ARG, "bytes is NULL");
+  if (op == HISA_OP_SPARSE_ATTENTION_KV4) return kv4_workspace(s, bytes);
   hisa_status e = check_shape(s, op != HISA_OP_FLAT_TOPK && op != HISA_OP_FLAT_TOPK_SAMPLED);
   if (e != HISA_OK) return e;
   switch (op) {
@@ -1093,6 +1114,176 @@ hisa_status hisa_sparse_attention(const void* q, const void* kv, const int32_t* 
   e = cuda_check(cudaLaunchKernelEx(&cfg, sparse_attn_kernel, kvm, ropem, p), "launch sparse_attn_kernel");
   if (e != HISA_OK) return e;
   return launch_check("sparse_attn_kernel");
+}
+
+}  // extern "C"
+
+// =================================================================== rotary, norms, 4-bit cache
+
+namespace {
+
+hisa_status check_rows(const void* x, int64_t xt, int64_t xh, const void* out, int64_t ot, int64_t oh, int64_t tokens,
+                       int32_t heads, int32_t dim, int32_t dtype) {
+  if (dtype != HISA_F32 && dtype != HISA_BF16) return fail(HISA_ERR_UNSUPPORTED, "rows must be fp32 or bf16");
+  if (tokens < 0 || heads < 1 || dim < 1) return fail(HISA_ERR_INVALID_ARG, "tokens must be >= 0, heads and dim >= 1");
+  if (dim > kRotaryMaxDim) return fail(HISA_ERR_UNSUPPORTED, "dim must be <= %d", kRotaryMaxDim);
+  if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return fail(HISA_ERR_INVALID_ARG, "strides must be >= 0");
+  // a row of out written by two (token, head) pairs would be a race
+  if ((tokens > 1 && ot < dim) || (heads > 1 && oh < dim))
+    return fail(HISA_ERR_INVALID_ARG, "out's rows overlap: its token and head strides must be >= dim");
+  if (x == out && tokens > 0 && ((tokens > 1 && xt != ot) || (heads > 1 && xh != oh)))
+    return fail(HISA_ERR_INVALID_ARG, "in place, out's strides must be x's");
+  return HISA_OK;
+}
+
+bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(n - 1)) == 0; }
+
+template <int DT>
+hisa_status launch_rotary_dt(const RotaryParams& p, int norm, cudaStream_t st) {
+  const int64_t blocks = ceil_div(p.rows, kRotaryWarps);
+  if (blocks > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
+  const unsigned g = static_cast<unsigned>(blocks);
+  switch (norm) {
+    case NORM_NONE: norm_rotary_rows_kernel<DT, NORM_NONE><<<g, 32 * kRotaryWarps, 0, st>>>(p); break;
+    case NORM_RMS: norm_rotary_rows_kernel<DT, NORM_RMS><<<g, 32 * kRotaryWarps, 0, st>>>(p); break;
+    default: norm_rotary_rows_kernel<DT, NORM_LAYER><<<g, 32 * kRotaryWarps, 0, st>>>(p); break;
+  }
+  return launch_check("norm_rotary_rows_kernel");
+}
+
+hisa_status run_rotary(const void* x, int64_t xt, int64_t xh, const int32_t* positions, const double* inv_freq,
+                       int64_t tokens, int32_t heads, int32_t dim, int32_t norm, int32_t norm_dim,
+                       const float* weight, const float* bias, float eps, int32_t rotary_dim, int32_t offset,
+                       int32_t interleaved, int32_t reverse, float amplitude, int32_t dtype, void* out, int64_t ot,
+                       int64_t oh, hisa_stream stream) {
+  hisa_status e = check_rows(x, xt, xh, out, ot, oh, tokens, heads, dim, dtype);
+  if (e != HISA_OK) return e;
+  if (rotary_dim < 2 || rotary_dim % 2 != 0 || offset < 0 || offset > dim || rotary_dim > dim - offset)
+    return fail(HISA_ERR_INVALID_ARG, "rotary_dim must be even, >= 2 and [offset, offset + rotary_dim) inside the row");
+  if (!std::isfinite(amplitude)) return fail(HISA_ERR_INVALID_ARG, "amplitude must be finite");
+  if (norm != NORM_NONE) {
+    if (norm != NORM_RMS && norm != NORM_LAYER) return fail(HISA_ERR_INVALID_ARG, "unknown norm %d", norm);
+    if (norm_dim < 1 || norm_dim > dim) return fail(HISA_ERR_INVALID_ARG, "norm_dim must be in [1, dim]");
+    if (norm == NORM_RMS && bias) return fail(HISA_ERR_INVALID_ARG, "the RMS norm has no bias");
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(HISA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  }
+  if (tokens == 0) return HISA_OK;
+  const int es = elem_bytes(dtype);
+  if (!x || !out || !positions || !inv_freq || (norm != NORM_NONE && !weight))
+    return fail(HISA_ERR_INVALID_ARG, "x, out, positions, inv_freq and weight must be non-NULL");
+  if (!aligned_to(x, es) || !aligned_to(out, es) || !aligned4(positions) || !aligned_to(inv_freq, 8) ||
+      !aligned4(weight) || !aligned4(bias))
+    return fail(HISA_ERR_INVALID_ARG, "x, out, positions, inv_freq, weight and bias must be aligned to their elements");
+  RotaryParams p{};
+  p.x = x; p.out = out; p.pos = positions; p.inv_freq = inv_freq; p.weight = weight; p.bias = bias;
+  p.x_token = xt; p.x_head = xh; p.out_token = ot; p.out_head = oh;
+  p.rows = tokens * heads; p.heads = heads; p.dim = dim; p.rot = rotary_dim; p.offset = offset; p.norm_dim = norm_dim;
+  // in place, features that nothing changes are not touched
+  const bool inplace = x == out;
+  p.first = inplace && norm == NORM_NONE ? offset : 0;
+  p.last = inplace ? std::max(norm == NORM_NONE ? 0 : norm_dim, offset + rotary_dim) : dim;
+  p.amplitude = amplitude; p.eps = eps; p.sign = reverse ? -1.f : 1.f;
+  p.interleaved = interleaved != 0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dtype == HISA_F32 ? launch_rotary_dt<DT_F32>(p, norm, st) : launch_rotary_dt<DT_BF16>(p, norm, st);
+}
+
+hisa_status check_kv4_rows(const void* rows, int64_t row_stride, const int32_t* slots, int64_t n, const void* cache,
+                           int64_t num_slots) {
+  if (n < 0 || num_slots < 1 || num_slots > INT32_MAX)
+    return fail(HISA_ERR_INVALID_ARG, "n must be >= 0 and num_slots in [1, 2^31)");
+  if (row_stride < kKv4Width || row_stride % 8 != 0)
+    return fail(HISA_ERR_INVALID_ARG, "row_stride must be a multiple of 8 and >= %d", kKv4Width);
+  if (n == 0) return HISA_OK;
+  if (!rows || !slots || !cache) return fail(HISA_ERR_INVALID_ARG, "rows, slots and cache must be non-NULL");
+  if (!aligned16(rows) || !aligned16(cache) || !aligned4(slots))
+    return fail(HISA_ERR_INVALID_ARG, "rows and cache must be 16-byte aligned, slots 4-byte aligned");
+  if (ceil_div(n, kKv4Warps) > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
+  return HISA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+hisa_status hisa_rotary(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                        const double* inv_freq, int64_t tokens, int32_t heads, int32_t dim, int32_t rotary_dim,
+                        int32_t offset, int32_t interleaved, int32_t reverse, float amplitude, int32_t dtype, void* out,
+                        int64_t out_token_stride, int64_t out_head_stride, hisa_stream stream) {
+  return run_rotary(x, x_token_stride, x_head_stride, positions, inv_freq, tokens, heads, dim, NORM_NONE, 0, nullptr,
+                    nullptr, 0.f, rotary_dim, offset, interleaved, reverse, amplitude, dtype, out, out_token_stride,
+                    out_head_stride, stream);
+}
+
+hisa_status hisa_norm_rotary(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                             const double* inv_freq, int64_t tokens, int32_t heads, int32_t dim, int32_t norm,
+                             int32_t norm_dim, const float* weight, const float* bias, float eps, int32_t rotary_dim,
+                             int32_t offset, int32_t interleaved, float amplitude, int32_t dtype, void* out,
+                             int64_t out_token_stride, int64_t out_head_stride, hisa_stream stream) {
+  if (norm != HISA_NORM_RMS && norm != HISA_NORM_LAYER) return fail(HISA_ERR_INVALID_ARG, "unknown norm %d", norm);
+  return run_rotary(x, x_token_stride, x_head_stride, positions, inv_freq, tokens, heads, dim, norm, norm_dim, weight,
+                    bias, eps, rotary_dim, offset, interleaved, 0, amplitude, dtype, out, out_token_stride,
+                    out_head_stride, stream);
+}
+
+hisa_status hisa_kv4_write(const void* rows, int64_t row_stride, const int32_t* slots, int64_t n, void* cache,
+                           int64_t num_slots, hisa_stream stream) {
+  hisa_status e = check_kv4_rows(rows, row_stride, slots, n, cache, num_slots);
+  if (e != HISA_OK || n == 0) return e;
+  Kv4RowParams p{slots, static_cast<uint8_t*>(cache), static_cast<uint8_t*>(const_cast<void*>(rows)), n, num_slots,
+                 row_stride * 2};
+  kv4_write_kernel<<<static_cast<unsigned>(ceil_div(n, kKv4Warps)), 32 * kKv4Warps, 0,
+                     reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return launch_check("kv4_write_kernel");
+}
+
+hisa_status hisa_kv4_read(const void* cache, int64_t num_slots, const int32_t* slots, int64_t n, void* rows,
+                          int64_t row_stride, hisa_stream stream) {
+  hisa_status e = check_kv4_rows(rows, row_stride, slots, n, cache, num_slots);
+  if (e != HISA_OK || n == 0) return e;
+  Kv4RowParams p{slots, static_cast<uint8_t*>(const_cast<void*>(cache)), static_cast<uint8_t*>(rows), n, num_slots,
+                 row_stride * 2};
+  kv4_read_kernel<<<static_cast<unsigned>(ceil_div(n, kKv4Warps)), 32 * kKv4Warps, 0,
+                    reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return launch_check("kv4_read_kernel");
+}
+
+hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t num_pages, int32_t page_size,
+                                      const int32_t* page_table, const int32_t* idx, int32_t batch,
+                                      int32_t num_queries, int32_t num_keys, int32_t heads, int32_t top_k, float scale,
+                                      void* o, float* lse, void* workspace, size_t ws_bytes, hisa_stream stream) {
+  hisa_status e = check_kv4_attn(batch, num_queries, heads, top_k);
+  if (e != HISA_OK) return e;
+  if (num_keys < 1 || num_pages < 1 || page_size < 1)
+    return fail(HISA_ERR_INVALID_ARG, "num_keys, num_pages and page_size must be >= 1");
+  if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX)
+    return fail(HISA_ERR_UNSUPPORTED, "num_pages * page_size must fit in int32");
+  if (!std::isfinite(scale)) return fail(HISA_ERR_INVALID_ARG, "scale must be finite");
+  if (!q || !cache || !page_table || !idx || !o || !lse)
+    return fail(HISA_ERR_INVALID_ARG, "q, cache, page_table, idx, o and lse must be non-NULL");
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned4(page_table) || !aligned4(idx) || !aligned4(lse))
+    return fail(HISA_ERR_INVALID_ARG,
+                "q, cache and o must be 16-byte aligned, page_table, idx and lse 4-byte aligned");
+  if (workspace && !aligned16(workspace)) return fail(HISA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+  const int64_t rows = static_cast<int64_t>(batch) * num_queries;
+  const int64_t blocks = rows * ceil_div(heads, kKv4SimtHeads);
+  if (blocks > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many (query, head) pairs");
+  Kv4AttnParams p{};
+  p.rows = rows; p.Q = num_queries; p.L = num_keys; p.heads = heads; p.top_k = top_k;
+  p.page_size = page_size; p.num_pages = num_pages;
+  p.pages_per_seq = static_cast<int>(ceil_div(num_keys, page_size));
+  p.scale = scale;
+  p.idx = idx; p.page_table = page_table; p.cache = static_cast<const uint8_t*>(cache);
+  p.q = static_cast<const uint16_t*>(q); p.o = static_cast<uint16_t*>(o); p.lse = lse;
+  int slots = 64;
+  while (slots < 2 * top_k) slots *= 2;
+  const size_t smem = kv4_simt_smem(slots);
+  e = cuda_check(cudaFuncSetAttribute(kv4_attn_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(smem)), "kv4_attn_simt attribute");
+  if (e != HISA_OK) return e;
+  kv4_attn_simt_kernel<<<static_cast<unsigned>(blocks), kKv4SimtThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
+      p, slots);
+  return launch_check("kv4_attn_simt_kernel");
 }
 
 }  // extern "C"

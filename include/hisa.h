@@ -92,8 +92,12 @@ enum {
   HISA_OP_FLAT_TOPK = 3,
   HISA_OP_FLAT_TOPK_SAMPLED = 4,
   HISA_OP_BLOCK_REFINE_TOPM = 5,
-  HISA_OP_INDEXER_FROM_HOST = 6
+  HISA_OP_INDEXER_FROM_HOST = 6,
+  HISA_OP_SPARSE_ATTENTION_KV4 = 7
 };
+
+/* norms of hisa_norm_rotary */
+enum { HISA_NORM_RMS = 1, HISA_NORM_LAYER = 2 };
 
 /*
  * Block pooling (HISA coarse stage input; HISA abstract, "pooled block
@@ -404,6 +408,115 @@ HISA_API hisa_status hisa_sparse_attention(const void* q, const void* kv, const 
                                            int32_t batch, int32_t num_queries, int32_t num_keys,
                                            int32_t heads, int32_t d_qk, int32_t d_v, int32_t top_k,
                                            float scale, void* o, float* lse, hisa_stream stream);
+
+/*
+ * Rotary positions.  Of each row x[t, h, :] (dim features) the features
+ * [offset, offset + rotary_dim) turn in pairs by the token's position:
+ *     angle_i = positions[t] * inv_freq[i]              i < rotary_dim / 2
+ *     (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * with (a, b) the features (2i, 2i+1) of the part when `interleaved`, else
+ * (i, i + rotary_dim / 2).  `reverse` turns by -angle: with the same amplitude
+ * the gradient of the rotation, with 1 / amplitude its inverse.  The other
+ * features are copied.  Scaled positions (long contexts) are scaled inv_freq
+ * and an amplitude.  The angle is exact to 2^-31 turns at every int32
+ * position; the products are fp32, rounded once to the dtype.
+ *   x          [tokens, heads, dim] HISA_F32 or HISA_BF16, features
+ *              contiguous, the other strides given in elements
+ *   positions  [tokens] int32;  inv_freq [rotary_dim / 2] fp64 (radians per
+ *              position), both device
+ *   out        [tokens, heads, dim] likewise; x itself with x's strides (only
+ *              the turned features are then touched), else no element of out
+ *              may be one of x
+ * Pointers are aligned to their element size (inv_freq 8, positions 4 bytes);
+ * 16-byte aligned rows run faster.  dim <= 1024, rotary_dim even and >= 2.
+ * tokens == 0 returns HISA_OK without a launch.
+ */
+HISA_API hisa_status hisa_rotary(const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                                 const int32_t* positions, const double* inv_freq, int64_t tokens,
+                                 int32_t heads, int32_t dim, int32_t rotary_dim, int32_t offset,
+                                 int32_t interleaved, int32_t reverse, float amplitude, int32_t dtype,
+                                 void* out, int64_t out_token_stride, int64_t out_head_stride,
+                                 hisa_stream stream);
+
+/*
+ * The norm of each row's features [0, norm_dim), then hisa_rotary's turn of
+ * [offset, offset + rotary_dim), in one pass (the two ranges may overlap):
+ *     HISA_NORM_RMS    y = x * weight / sqrt(mean(x^2) + eps)
+ *     HISA_NORM_LAYER  y = (x - mean) * weight / sqrt(var + eps) + bias
+ * weight and bias [norm_dim] fp32 (bias NULL, and with RMS it must be: none).
+ * The norm and the products are fp32, rounded once to the dtype.  Arguments
+ * otherwise as for hisa_rotary; eps >= 0.
+ */
+HISA_API hisa_status hisa_norm_rotary(const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                                      const int32_t* positions, const double* inv_freq, int64_t tokens,
+                                      int32_t heads, int32_t dim, int32_t norm, int32_t norm_dim,
+                                      const float* weight, const float* bias, float eps,
+                                      int32_t rotary_dim, int32_t offset, int32_t interleaved,
+                                      float amplitude, int32_t dtype, void* out,
+                                      int64_t out_token_stride, int64_t out_head_stride,
+                                      hisa_stream stream);
+
+/*
+ * The 4-bit latent cache.  One latent row (the kv row of
+ * hisa_sparse_attention: 512 latent + 64 positional features, bf16) is kept
+ * as a record of 416 bytes instead of 1152:
+ *   bytes [0, 256)    512 codes n in -7..7, two's complement nibbles: the
+ *                     32-bit little-endian word i holds features 8i .. 8i+7,
+ *                     the even ones in its low half, the odd ones in its high
+ *                     half, each half from its lowest nibble up
+ *   bytes [256, 288)  a scale code c for each 16 features,
+ *                     s = (1 + (c & 7) / 8) * 2^((c >> 3) - 20)
+ *   bytes [288, 416)  the 64 positional features in bf16
+ * s is the smallest such value with 7 s >= max|x| of the group (the largest,
+ * 3840, if none is: the group saturates) and n = x / s to the nearest, ties to
+ * even; a NaN counts as 0.  A feature reads back as n * s, exact in bf16 and at
+ * most s / 2 off.
+ *   cache  [num_slots, 416] bytes, 16-byte aligned: a cache of pages
+ *          [num_pages, page_size] has num_pages * page_size slots, the slot of
+ *          row r of page p being p * page_size + r
+ *   slots  [n] int32 (device)
+ *   rows   [n, 576] bf16, 16-byte aligned, row_stride elements apart (a
+ *          multiple of 8, >= 576)
+ * hisa_kv4_write quantises rows[i] into record slots[i]; a slot below 0 is
+ * skipped (a padded token), every other record is left as it was.  Distinct
+ * rows go to distinct slots: a slot named twice holds parts of either row.
+ * hisa_kv4_read writes what record slots[i] stands for to rows[i], zeros for a
+ * slot below 0.  A slot past num_slots is skipped (read: zeros) and the device
+ * status word reports HISA_ERR_INVALID_ARG.  n == 0 returns HISA_OK without a
+ * launch.
+ */
+HISA_API hisa_status hisa_kv4_write(const void* rows, int64_t row_stride, const int32_t* slots, int64_t n,
+                                    void* cache, int64_t num_slots, hisa_stream stream);
+HISA_API hisa_status hisa_kv4_read(const void* cache, int64_t num_slots, const int32_t* slots, int64_t n,
+                                   void* rows, int64_t row_stride, hisa_stream stream);
+
+/*
+ * hisa_sparse_attention over the 4-bit latent cache in pages: the same
+ * formula, index rows and empty-set rule, with kv[s] the row that the record
+ * of position s stands for, row s % page_size of page
+ * page_table[b, s / page_size].
+ *   q           [batch, Q, heads, 576] bf16, heads >= 1
+ *   cache       [num_pages, page_size, 416] bytes (hisa_kv4_write)
+ *   page_table  [batch, ceil(L / page_size)] int32, L = num_keys
+ *   idx         [batch, Q, top_k] int32, top_k <= 4096
+ *   o           [batch, Q, heads, 512] bf16;  lse [batch, Q, heads] fp32
+ * Entries of idx outside [0, L) and repeats are dropped.  A page that is
+ * needed and lies outside [0, num_pages) is not dereferenced: the position is
+ * dropped and the device status word reports HISA_ERR_INVALID_ARG.
+ * num_pages * page_size must fit in int32.
+ * Workspace: optional, 16-byte aligned.
+ * hisa_workspace_size(HISA_OP_SPARSE_ATTENTION_KV4), from the shape's batch,
+ * num_queries, heads and top_k, is nonzero where there are few queries (a
+ * decode step); given that much, each query's keys are split over several
+ * pairs of SMs and the parts joined.  NULL (or less) runs each query whole.
+ * The two agree to rounding.
+ */
+HISA_API hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t num_pages,
+                                               int32_t page_size, const int32_t* page_table,
+                                               const int32_t* idx, int32_t batch, int32_t num_queries,
+                                               int32_t num_keys, int32_t heads, int32_t top_k, float scale,
+                                               void* o, float* lse, void* workspace, size_t ws_bytes,
+                                               hisa_stream stream);
 
 /* Workspace bytes that let `op` run on `shape` in one pass (0 if none). */
 HISA_API hisa_status hisa_workspace_size(int32_t op, const hisa_shape* shape,
