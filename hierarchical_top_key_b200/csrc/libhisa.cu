@@ -48,6 +48,7 @@ hisa_status cuda_check(cudaError_t e, const char* what) {
 hisa_status launch_check(const char* what) { return cuda_check(cudaGetLastError(), what); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int elem_bytes(int dt) { return dt == HISA_F32 ? 4 : dt == HISA_BF16 ? 2 : 1; }
@@ -335,11 +336,22 @@ hisa_status check_kv4_attn(int32_t batch, int32_t num_queries, int32_t heads, in
   return HISA_OK;
 }
 
+// Parts of each row's keys: as many as give every pair of SMs one work item,
+// at least one 64-key tile each.
+int kv4_parts(int64_t rows, int32_t heads, int32_t top_k) {
+  const int64_t items = rows * ceil_div(heads, kAttnHeads);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / items, ceil_div(top_k, kAttnTileN))));
+}
+
+size_t kv4_part_bytes(int64_t rows, int32_t heads, int parts) {
+  return parts == 1 ? 0 : static_cast<size_t>(rows) * heads * parts * (kAttnDv + 1) * 4;
+}
+
 hisa_status kv4_workspace(const hisa_shape* s, size_t* bytes) {
   if (!s) return fail(HISA_ERR_INVALID_ARG, "shape is NULL");
   hisa_status e = check_kv4_attn(s->batch, s->num_queries, s->heads, s->top_k);
   if (e != HISA_OK) return e;
-  *bytes = 0;
+  *bytes = kv4_part_bytes(rows_of(s), s->heads, kv4_parts(rows_of(s), s->heads, s->top_k));
   return HISA_OK;
 }
 
@@ -1196,8 +1208,8 @@ hisa_status check_kv4_rows(const void* rows, int64_t row_stride, const int32_t* 
     return fail(HISA_ERR_INVALID_ARG, "row_stride must be a multiple of 8 and >= %d", kKv4Width);
   if (n == 0) return HISA_OK;
   if (!rows || !slots || !cache) return fail(HISA_ERR_INVALID_ARG, "rows, slots and cache must be non-NULL");
-  if (!aligned16(rows) || !aligned16(cache) || !aligned4(slots))
-    return fail(HISA_ERR_INVALID_ARG, "rows and cache must be 16-byte aligned, slots 4-byte aligned");
+  if (!aligned16(rows) || !aligned32(cache) || !aligned4(slots))
+    return fail(HISA_ERR_INVALID_ARG, "rows must be 16-byte, cache 32-byte and slots 4-byte aligned");
   if (ceil_div(n, kKv4Warps) > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
   return HISA_OK;
 }
@@ -1261,29 +1273,52 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
   if (!std::isfinite(scale)) return fail(HISA_ERR_INVALID_ARG, "scale must be finite");
   if (!q || !cache || !page_table || !idx || !o || !lse)
     return fail(HISA_ERR_INVALID_ARG, "q, cache, page_table, idx, o and lse must be non-NULL");
-  if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned4(page_table) || !aligned4(idx) || !aligned4(lse))
+  if (!aligned16(q) || !aligned32(cache) || !aligned16(o) || !aligned4(page_table) || !aligned4(idx) || !aligned4(lse))
     return fail(HISA_ERR_INVALID_ARG,
-                "q, cache and o must be 16-byte aligned, page_table, idx and lse 4-byte aligned");
+                "q and o must be 16-byte, cache 32-byte, page_table, idx and lse 4-byte aligned");
   if (workspace && !aligned16(workspace)) return fail(HISA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
   const int64_t rows = static_cast<int64_t>(batch) * num_queries;
-  const int64_t blocks = rows * ceil_div(heads, kKv4SimtHeads);
-  if (blocks > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many (query, head) pairs");
+  const int64_t slices = ceil_div(heads, kAttnHeads);
+  const int parts = workspace && ws_bytes >= kv4_part_bytes(rows, heads, kv4_parts(rows, heads, top_k))
+                        ? kv4_parts(rows, heads, top_k) : 1;
+  if (rows * slices * 2 > INT32_MAX || rows * heads > INT32_MAX)
+    return fail(HISA_ERR_UNSUPPORTED, "too many (query, head) pairs");
   Kv4AttnParams p{};
   p.rows = rows; p.Q = num_queries; p.L = num_keys; p.heads = heads; p.top_k = top_k;
   p.page_size = page_size; p.num_pages = num_pages;
   p.pages_per_seq = static_cast<int>(ceil_div(num_keys, page_size));
-  p.scale = scale;
+  p.slots = 64;
+  while (p.slots < 2 * top_k) p.slots *= 2;
+  p.slices = static_cast<int>(slices); p.parts = parts;
+  // the kernel's masked logits are -inf, which a scale of 0 would turn into NaN
+  p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
+  p.q_keep = scale == 0.f ? 0u : ~0u;
+  p.q_flip = scale < 0.f ? 0x80008000u : 0u;
   p.idx = idx; p.page_table = page_table; p.cache = static_cast<const uint8_t*>(cache);
   p.q = static_cast<const uint16_t*>(q); p.o = static_cast<uint16_t*>(o); p.lse = lse;
-  int slots = 64;
-  while (slots < 2 * top_k) slots *= 2;
-  const size_t smem = kv4_simt_smem(slots);
-  e = cuda_check(cudaFuncSetAttribute(kv4_attn_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem)), "kv4_attn_simt attribute");
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o ? p.part_o + rows * heads * parts * kAttnDv : nullptr;
+  e = cuda_check(cudaFuncSetAttribute(kv4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(kKv4SmemBytes)), "kv4_attn attribute");
   if (e != HISA_OK) return e;
-  kv4_attn_simt_kernel<<<static_cast<unsigned>(blocks), kKv4SimtThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
-      p, slots);
-  return launch_check("kv4_attn_simt_kernel");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * slices * parts * 2));
+  cfg.blockDim = dim3(kKv4Threads);
+  cfg.dynamicSmemBytes = kKv4SmemBytes;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_attn_kernel, p), "launch kv4_attn_kernel");
+  if (e != HISA_OK) return e;
+  e = launch_check("kv4_attn_kernel");
+  if (e != HISA_OK || parts == 1) return e;
+  kv4_join_kernel<<<static_cast<unsigned>(rows * heads), 128, 0, cfg.stream>>>(p);
+  return launch_check("kv4_join_kernel");
 }
 
 }  // extern "C"

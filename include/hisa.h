@@ -471,7 +471,7 @@ HISA_API hisa_status hisa_norm_rotary(const void* x, int64_t x_token_stride, int
  * 3840, if none is: the group saturates) and n = x / s to the nearest, ties to
  * even; a NaN counts as 0.  A feature reads back as n * s, exact in bf16 and at
  * most s / 2 off.
- *   cache  [num_slots, 416] bytes, 16-byte aligned: a cache of pages
+ *   cache  [num_slots, 416] bytes, 32-byte aligned: a cache of pages
  *          [num_pages, page_size] has num_pages * page_size slots, the slot of
  *          row r of page p being p * page_size + r
  *   slots  [n] int32 (device)

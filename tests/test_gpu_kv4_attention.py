@@ -51,10 +51,10 @@ class Case:
         hb.hisa_kv4_write(t, slot, self.cache)
         self.kv[b, s] = hb.hisa_kv4_read(self.cache, slot).float().cpu().numpy()[0]
 
-    def run(self, q, idx, **kw):
+    def run(self, q, idx, scale=SCALE):
         hb = _hb()
         o, lse = hb.hisa_sparse_attention_kv4(q.cuda(), self.cache, self.table.cuda(), torch.from_numpy(idx).cuda(),
-                                              scale=SCALE, num_keys=self.L, **kw)
+                                              scale=scale, num_keys=self.L)
         hb.get_status()
         return o, lse
 
@@ -188,6 +188,16 @@ def test_large_logits_and_jumps_of_the_maximum(lib):
     o, lse = c.run(q, idx)
     c.check(q, idx, o, lse, "planted maxima")
     assert np.median(lse.cpu().numpy()[0, 0]) > 20.0
+
+
+@pytest.mark.parametrize("factor", [0.0, -1.0, 2.0 ** -120])
+def test_scales(lib, factor):
+    """A scale of 0 (every key alike), a negative and a tiny one: as the query times the factor."""
+    c = Case(1, 300, 64, 13)
+    q = _q(1, 2, 128, 13)
+    idx = synthetic.random_index_rows(1, 2, 300, 100, np.full((1, 2), 300), seed=13)
+    o, lse = c.run(q, idx, scale=SCALE * factor)
+    c.check((q.float() * factor).to(torch.bfloat16), idx, o, lse, f"factor={factor}")
 
 
 def test_pages_outside_the_cache_are_reported(lib):
