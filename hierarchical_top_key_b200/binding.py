@@ -577,7 +577,8 @@ def hisa_sparse_attention_kv4(q, cache, page_table, idx, *, scale: float, num_ke
     """hisa_sparse_attention over the 4-bit paged cache: q [batch, Q, H, 576] bf16,
     cache [num_pages, page_size, 416] uint8, page_table [batch,
     ceil(num_keys / page_size)] int32, idx [batch, Q, top_k] int32 ->
-    (o [batch, Q, H, 512] bf16, lse [batch, Q, H] fp32)."""
+    (o [batch, Q, H, 512] bf16, lse [batch, Q, H] fp32).  A smaller workspace
+    than hisa_workspace_size runs the queries in chunks that fit."""
     _need(q, "q", 4)
     _check_kv4(cache)
     _need(page_table, "page_table", 2)
@@ -594,14 +595,15 @@ def hisa_sparse_attention_kv4(q, cache, page_table, idx, *, scale: float, num_ke
     with _device_of(q):
         o = torch.empty((b, Q, H, KV4_LATENT), dtype=torch.bfloat16, device=q.device)
         lse = torch.empty((b, Q, H), dtype=torch.float32, device=q.device)
-        need = workspace_size(OP_ATTENTION_KV4, Shape(b, num_keys, Q, H, 0, 0, 0, idx.shape[2], HISA_BF16))
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = _workspace(need, q.device)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws = workspace
+        if ws is None:
+            ws = _workspace(workspace_size(OP_ATTENTION_KV4, Shape(b, num_keys, Q, H, 0, 0, 0, idx.shape[2], HISA_BF16)),
+                            q.device)
         _check(load().hisa_sparse_attention_kv4(q.data_ptr(), cache.data_ptr(), cache.shape[0], cache.shape[1],
                                                 page_table.data_ptr(), idx.data_ptr(), b, Q, num_keys, H, idx.shape[2],
-                                                float(scale), o.data_ptr(), lse.data_ptr(), _ptr(workspace), nbytes,
-                                                _stream()), "hisa_sparse_attention_kv4")
+                                                float(scale), o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                                ws.numel() * ws.element_size(), _stream()),
+               "hisa_sparse_attention_kv4")
     return o, lse
 
 

@@ -25,9 +25,6 @@ namespace hisa {
 constexpr int kKv4Latent = 512, kKv4Rope = 64, kKv4Width = kKv4Latent + kKv4Rope, kKv4Group = 16;
 constexpr int kKv4ScaleAt = 256, kKv4RopeAt = 288, kKv4Record = 416;
 
-// Scale code -> the bf16 bits of 16 s (the exponent field starts 4 up).
-__device__ __forceinline__ uint32_t kv4_scale16_bits(uint32_t c) { return (c << 4) + ((127u - 20u + 4u) << 7); }
-
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -52,10 +49,12 @@ __device__ __forceinline__ void kv4_decode8(uint32_t w, uint32_t s16, uint32_t m
   out[3] = hfma2_bf16(((w >> 9) & kMask) ^ kFlip, s16, m24);
 }
 
-// (16 s, -24 s) of a scale code as packed bf16 pairs.
-__device__ __forceinline__ void kv4_scales(uint32_t code, uint32_t& s16, uint32_t& m24) {
-  const uint32_t b = kv4_scale16_bits(code);
-  s16 = b | (b << 16);
+// (16 s, -24 s) of scale code g of the four in `codes`, as packed bf16 pairs:
+// the code is the exponent's low bits and the upper mantissa bits of s in
+// bf16, and 16 s has its exponent 4 up.
+__device__ __forceinline__ void kv4_scales(uint32_t codes, int g, uint32_t& s16, uint32_t& m24) {
+  constexpr uint32_t kBias = (127u - 20u + 4u) << 7;
+  s16 = __byte_perm(codes, 0u, 0x4040u + 0x0101u * g) * 16u + (kBias | (kBias << 16));
   m24 = hmul2_bf16(s16, 0xBFC0BFC0u);          // * -1.5
 }
 
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv4_read_kernel(const Kv4RowPa
     const uint8_t* src = p.cache + slot * kKv4Record;
     const uint2 w = *reinterpret_cast<const uint2*>(src + lane * 8);
     uint32_t s16, m24;
-    kv4_scales(src[kKv4ScaleAt + lane], s16, m24);
+    kv4_scales(src[kKv4ScaleAt + lane], 0, s16, m24);
     uint32_t d[4];
     kv4_decode8(w.x, s16, m24, d);
 #pragma unroll

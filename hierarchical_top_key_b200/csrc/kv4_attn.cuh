@@ -9,27 +9,43 @@
 //     lse[t, h]   = log sum_j exp(logit[h, j])          (natural log)
 // and an empty set gives o = 0, lse = -inf.
 //
-// The pair of CTAs of sparse_attn.cuh: 128 heads are the M of every MMA, each
-// CTA holds half the features (288 of the row's 576, 256 of the output's 512),
-// computes its part of a 64-key tile's logits, the parts cross through
-// distributed shared memory, and both run the same softmax.  What differs:
-//   - the keys are not gathered by TMA but by eight warps that load a record's
-//     codes, turn them into bf16 in registers (kv4.cuh) and store them in the
-//     swizzled layout the MMA reads: 4-bit rows cross L2 and HBM, bf16 rows
-//     exist only in shared memory;
-//   - eight softmax warps instead of four, two to a head row (32 keys each);
-//   - any number of heads (a slice's missing heads are zero rows), keys in
-//     pages, and few queries split over the keys: part i of a row takes a
-//     contiguous run of its tiles and writes an fp32 output with its own lse;
-//     a second kernel joins the parts.
+// 1. kv4_select_kernel turns each index row into the list of its records.
+// 2. kv4_attn_kernel: 128 heads are the M of every MMA.  Their 512 fp32 output
+//    columns fill an SM's TMEM, so a pair of CTAs (a cluster) shares a query:
+//    CTA r holds output columns 256r .. 256r+255.  The 64-key tiles are dealt
+//    out in turn: the owner of a tile computes its whole logits (K = 576) and
+//    softmax weights P, and puts P (bf16, 16 KB) into its own shared memory
+//    and its peer's; both add P . V for their half of the features.  Nothing
+//    is computed twice, and what crosses between the SMs is 8 KB a tile each
+//    way (exchanging fp32 partial logits instead takes 32 KB, and the writes
+//    into the peer's memory then hold up every other shared-memory access).
+//    Eight producer warps load the records' codes, turn them into bf16 in
+//    registers and store them in the swizzled layout the MMA reads: 4-bit rows
+//    cross L2 and HBM, bf16 rows exist only in shared memory.  An owned tile
+//    needs the whole row, the peer's tile only this CTA's value half.
+// 3. Few queries are split over the keys: part i of a row takes a contiguous
+//    run of its tiles and writes an fp32 output with its own lse;
+//    kv4_join_kernel joins the parts.
 //
-// Warp roles (18 warps):
+// Softmax reference.  P of a tile is exp2(logit - m) for a reference m per head
+// row that need not be the maximum: fp32 sums and bf16 weights keep their
+// relative precision at any size.  The maximum over the query's first 32 keys
+// serves the whole query unless a later logit exceeds it by more than 2^64
+// (sums then stay below 2^64 * 2^12 keys * 2^15, the largest value).  Only the
+// warp that meets it moves its m; weights come with the m they were made with,
+// and a mark where that has moved; before the MMA of marked weights the output
+// or the weights are scaled to one reference.
+//
+// Warp roles (26 warps a CTA, a persistent pair over queries):
 //   warp 0       TMEM owner, logit MMA issuer (one thread)
 //   warp 1       output MMA issuer (one thread)
-//   warps 2..9   key producers: 8 rows of every tile each
-//   warps 10..17 softmax: group g = 0, 1 (four warps each, a thread a head
-//                row) has keys 32g .. 32g+31 of every tile and columns
-//                128g .. 128g+127 of this CTA's output
+//   warps 2..13  producers, three teams of four: the query, and the value
+//                half of the peer's tiles; the value half of the own tiles;
+//                the rest of the own tiles
+//   warps 14..21 softmax of the own tiles: group g has keys 32g .. 32g+31, a
+//                thread a head row
+//   warps 22..25 the output, and the scaling above
+// Own tiles are numbered u, the peer's v, through all of a pair's queries.
 // Every wait is bounded; a timeout sets the CTA's abort flag and the status
 // word, and the peer CTA's waits on it then time out too.
 #pragma once
@@ -42,169 +58,353 @@ namespace hisa {
 constexpr int kKv4MaxK = 4096;                 // longest index row
 
 struct Kv4AttnParams {
-  int64_t rows;              // batch * Q
-  int Q, L, heads, top_k;
-  int page_size, pages_per_seq, num_pages;
-  int slots;                 // the selection's table: a power of two >= 2 * top_k
+  int Q, L, heads, top_k, list_ld;
+  int page_size, page_shift, pages_per_seq, num_pages;   // page_shift: log2(page_size), or -1
   int slices, parts;         // slices of 128 heads; parts of a row's keys
-  float scale_log2;          // |softmax scale| * log2(e)
-  uint32_t q_keep, q_flip;   // the query is (q & keep) ^ flip: its sign bits for a negative scale, 0 and scale 1 for 0
+  int64_t row0;              // the first query of this launch (of the chunk its workspace holds)
+  int64_t items;             // (queries of this launch) * slices * parts
+  float scale_log2;          // |softmax scale| * log2(e), 1 for a scale of 0
+  int sign;                  // of the scale: the logits are multiplied by it unless it is 1
   const int32_t* idx;        // [rows, top_k]
   const int32_t* page_table; // [batch, pages_per_seq]
   const uint8_t* cache;      // [num_pages, page_size, 416]
   const uint16_t* q;         // [rows, heads, 576] bf16
   uint16_t* o;               // [rows, heads, 512] bf16
   float* lse;                // [rows, heads]
-  float* part_o;             // [rows, heads, parts, 512] when parts > 1
-  float* part_lse;           // [rows, heads, parts]
+  int32_t* count;            // [queries of this launch]: records of each list
+  int32_t* list;             // [queries of this launch, list_ld]
+  float* part_o;             // [queries of this launch, heads, parts, 512] when parts > 1
+  float* part_lse;           // [queries of this launch, heads, parts]
 };
 
-// The records of one query's selected positions, in `list` (kKv4MaxK places,
-// also the scratch) in the order of the index row; returns their number.
-// A hash table of places maps each position to the first place of the row
-// that holds it (the result does not depend on the order of the atomics); a
-// place is kept when it is that one.  A position whose page is outside the
-// cache is dropped and reported.  Every thread of the block calls it; `table`
-// holds `slots` >= 2 * top_k (a power of two) words, `scan` a word per warp
-// and one more.
-template <int THREADS>
-__device__ __forceinline__ int kv4_select(const Kv4AttnParams& p, int64_t row, int32_t* list, uint32_t* table, int slots,
-                                          int* scan) {
-  constexpr int kPer = (kKv4MaxK + THREADS - 1) / THREADS;
-  static_assert(kPer <= 32, "one keep bit per place of a thread's run");
+// ---------------------------------------------------------------- selection
+
+constexpr int kKv4SelThreads = 512, kKv4SelWarps = kKv4SelThreads / 32;
+constexpr int kKv4Per = kKv4MaxK / kKv4SelThreads;        // places of an index row per thread
+
+// Words of the dedup table: four slots a place keep the probe chains short
+// (a chain is as long for a warp as for its unluckiest lane: at 1.5 slots a
+// place the chains were most of the kernel's time).
+__host__ __device__ inline uint32_t kv4_table_slots(int top_k) { return 4u * static_cast<uint32_t>(top_k) + 64u; }
+inline size_t kv4_select_smem(int top_k) { return (kv4_table_slots(top_k) + (top_k + 3) / 4 * 4) * 4; }
+
+// One block per query: the records of its selected positions, in the order of
+// the index row.  A hash table of places maps each position to the first place
+// of the row that holds it (the result does not depend on the order of the
+// atomics); a place is kept when it is that one.  A position whose page is
+// outside the cache is dropped and reported.  Thread t has places t, t + 512,
+// ...: all its loads are in flight together.
+__global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4AttnParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(16) int count[kKv4Per * kKv4SelWarps], place[kKv4Per * kKv4SelWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.top_k;
-  const int per = (K + THREADS - 1) / THREADS;
-  const int lo = min(K, tid * per), hi = min(K, lo + per);
+  const int64_t row = p.row0 + blockIdx.x;
+  uint32_t* table = reinterpret_cast<uint32_t*>(smem_raw);
+  const uint32_t slots = kv4_table_slots(K);
+  int32_t* pos = reinterpret_cast<int32_t*>(table + slots);
   const int32_t* irow = p.idx + row * K;
   const int32_t* pages = p.page_table + (row / p.Q) * p.pages_per_seq;
-  const int shift = 33 - __ffs(slots);                  // 32 - log2(slots)
-  for (int i = tid; i < slots / 4; i += THREADS) reinterpret_cast<uint4*>(table)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-  for (int i = lo; i < hi; ++i) {
-    const int x = __ldg(irow + i);
-    list[i] = x < p.L ? x : -1;                         // negative: not a key
+  int v[kKv4Per], rec[kKv4Per];
+#pragma unroll
+  for (int u = 0; u < kKv4Per; ++u) {
+    const int at = u * kKv4SelThreads + tid;
+    const int x = at < K ? __ldg(irow + at) : -1;
+    v[u] = x < p.L ? x : -1;                            // negative: not a key
+  }
+  for (uint32_t i = tid; i < slots / 4; i += kKv4SelThreads)
+    reinterpret_cast<uint4*>(table)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+#pragma unroll
+  for (int u = 0; u < kKv4Per; ++u) {
+    const int at = u * kKv4SelThreads + tid;
+    if (at < K) pos[at] = v[u];
+    rec[u] = -1;
+    if (v[u] >= 0) {
+      const int pg = p.page_shift >= 0 ? v[u] >> p.page_shift : v[u] / p.page_size;
+      const int page = __ldg(pages + pg);
+      if (page >= 0 && page < p.num_pages) {
+        rec[u] = page * p.page_size + (v[u] - pg * p.page_size);
+      }
+    }
   }
   __syncthreads();
-  int at[kPer];
+  // every round tries all open places of the thread at once; a place that
+  // finds another position in its slot goes to the next.  It ends: there are
+  // more slots than places.
+  uint32_t open = 0;
+  int at[kKv4Per];
 #pragma unroll
-  for (int u = 0; u < kPer; ++u) {
+  for (int u = 0; u < kKv4Per; ++u) {
     at[u] = -1;
-    if (lo + u < hi) {
-      const int v = list[lo + u];
-      if (v >= 0) {
-        // open addressing; at most top_k distinct positions in twice as many slots
-        uint32_t hs = (static_cast<uint32_t>(v) * 0x9E3779B1u) >> shift;
-        for (int probe = 0; probe < slots; ++probe) {
-          const uint32_t prev = atomicCAS(&table[hs], ~0u, static_cast<uint32_t>(lo + u));
-          if (prev == ~0u) break;
-          if (list[prev] == v) {
-            atomicMin(&table[hs], static_cast<uint32_t>(lo + u));
-            break;
-          }
-          hs = (hs + 1) & (slots - 1);
-        }
-        at[u] = static_cast<int>(hs);
+    if (v[u] >= 0) {
+      open |= 1u << u;
+      at[u] = static_cast<int>(__umulhi(static_cast<uint32_t>(v[u]) * 0x9E3779B1u, slots));
+    }
+  }
+  while (open) {
+    uint32_t prev[kKv4Per];
+#pragma unroll
+    for (int u = 0; u < kKv4Per; ++u)
+      if (open >> u & 1u) prev[u] = atomicCAS(&table[at[u]], ~0u, static_cast<uint32_t>(u * kKv4SelThreads + tid));
+#pragma unroll
+    for (int u = 0; u < kKv4Per; ++u) {
+      if (!(open >> u & 1u)) continue;
+      if (prev[u] == ~0u) {
+        open &= ~(1u << u);
+      } else if (pos[prev[u]] == v[u]) {
+        atomicMin(&table[at[u]], static_cast<uint32_t>(u * kKv4SelThreads + tid));
+        open &= ~(1u << u);
+      } else {
+        at[u] = at[u] + 1 == static_cast<int>(slots) ? 0 : at[u] + 1;
       }
     }
   }
   __syncthreads();
   uint32_t keep = 0;
-  int rec[kPer];
 #pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    rec[u] = 0;
-    if (at[u] >= 0 && table[at[u]] == static_cast<uint32_t>(lo + u)) {
-      const int v = list[lo + u];
-      const int pg = v / p.page_size;
-      const int page = __ldg(pages + pg);
-      if (page >= 0 && page < p.num_pages) {
-        keep |= 1u << u;
-        rec[u] = page * p.page_size + (v - pg * p.page_size);
-      } else {
-        record_status(HISA_ERR_INVALID_ARG);
-      }
+  for (int u = 0; u < kKv4Per; ++u) {
+    bool k = at[u] >= 0 && table[at[u]] == static_cast<uint32_t>(u * kKv4SelThreads + tid);
+    if (k && rec[u] < 0) {
+      record_status(HISA_ERR_INVALID_ARG);
+      k = false;
     }
+    const uint32_t all = __ballot_sync(kFull, k);
+    if (k) keep |= 1u << u;
+    if (lane == 0) count[u * kKv4SelWarps + warp] = __popc(all);
   }
-  const int cnt = __popc(keep);
-  int incl = cnt;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(kFull, incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  int base = 0, total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int c = scan[w];
-    if (w < warp) base += c;
-    total += c;
-  }
-  int pos = base + incl - cnt;
+  static_assert(kKv4Per * kKv4SelWarps == 128, "four counts a lane");
+  if (warp == 0) {
+    const int4 c = reinterpret_cast<const int4*>(count)[lane];
+    int incl = c.x + c.y + c.z + c.w;
+    const int mine = incl;
 #pragma unroll
-  for (int u = 0; u < kPer; ++u)
-    if (keep & (1u << u)) list[pos++] = rec[u];
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(kFull, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const int base = incl - mine;
+    reinterpret_cast<int4*>(place)[lane] = make_int4(base, base + c.x, base + c.x + c.y, base + c.x + c.y + c.z);
+    if (lane == 31) p.count[blockIdx.x] = incl;
+  }
   __syncthreads();
-  return total;
+  int32_t* out = p.list + static_cast<int64_t>(blockIdx.x) * p.list_ld;
+#pragma unroll
+  for (int u = 0; u < kKv4Per; ++u) {
+    const uint32_t all = __ballot_sync(kFull, (keep >> u) & 1u);
+    if ((keep >> u) & 1u) out[place[u * kKv4SelWarps + warp] + __popc(all & ((1u << lane) - 1u))] = rec[u];
+  }
 }
 
-// ---------------------------------------------------------------- tensor cores
+// ---------------------------------------------------------------- shared memory, TMEM
 
-constexpr int kKv4Threads = 576;
-constexpr int kKv4ProdBase = 64, kKv4ProdWarps = 8;    // warps 2..9
-constexpr int kKv4SoftBase = 320;                      // warps 10..17
-static_assert(kKv4ProdWarps * 8 == kAttnTileN, "8 rows a producer warp");
+constexpr int kKv4Threads = 832;
+constexpr int kKv4ProdBase = 64;               // warps 2..13
+constexpr int kKv4SoftBase = 448;              // warps 14..21
+constexpr int kKv4CorrBase = 704;              // warps 22..25
+
+// TMEM columns: one logit tile, six of the query's nine 64-feature panels (2
+// bf16 a column), the output
+constexpr uint32_t kKv4TmemS = 0, kKv4TmemQ = 64, kKv4TmemO = 256;
+constexpr int kKv4QPanels = 6;                 // in TMEM; the last two latent panels and the positional one in shared memory
+
+constexpr uint32_t kKv4Panel = kAttnTileN * 128;          // 64 keys x 64 features
+constexpr uint32_t kKv4QPanel = kAttnHeads * 128;         // 128 heads x 64 features
+constexpr uint32_t kKv4V = 4 * kKv4Panel;                 // a tile's value half
+constexpr uint32_t kKv4Kx = 5 * kKv4Panel;                // an owned tile's other half and positional panel
+constexpr uint32_t kKv4P = kAttnHeads * kAttnTileN * 2;   // a tile's weights
 
 struct Kv4Smem {
-  uint64_t q_full;
-  uint64_t kv_full[kAttnStages], kv_empty[kAttnStages];
+  uint64_t q_full, q_free, o_empty;            // a query is in place; its last own logits are done; its output has been read
+  uint64_t kx_full, vo_full[2], vo_empty[2];   // own tiles (the rest of a row: kx; s_full frees it)
+  uint64_t vr_full, vr_empty;                  // the peer's tiles
   uint64_t s_full, s_empty;
-  uint64_t p_full, pv_done;
-  uint64_t x_full[2][2];         // partial logits of the peer CTA: [tile parity][key half]
-  uint64_t pair[4];              // the two warps of a quarter of the head rows
-  uint64_t drain[2];             // one per MMA issuer
+  uint64_t p_own, p_peer, p_free;              // weights of an own tile, of a peer's tile; both CTAs have used mine
+  uint64_t first_full[2];                      // the query's reference, by query parity
+  uint64_t ctl, fix_done;                      // to the output warps: scale, or a query is done; their answer
+  uint64_t fin_own, fin_peer, fin_free;        // a query's sums
+  uint64_t drain[2];                           // one per MMA issuer
   uint32_t tmem_base;
   int abort_flag;
-  int scan[kKv4Threads / 32];
-  float red[2][2][kAttnHeads];   // [parity][group]: a row's maximum (at the end its sum) over the group's keys
+  int command;                                 // to the output warps
+  __align__(16) uint32_t moved[2][8];                        // [own, peer][softmax warp]: 1 + the tile whose reference that warp moved
+  float m_own[2][kAttnHeads], m_peer[2][kAttnHeads];   // references of the weights in place: [key half]
+  float m_first[2][kAttnHeads];                // [query parity]
+  float fin[2][2][2][kAttnHeads];              // [own, peer][key half][sum, reference]
 };
+enum : int { kKv4Done = 0, kKv4Scale = 1, kKv4First = 2, kKv4Peer = 4 };   // flags of `command`
 
-// The barriers and the row maxima, then the stages (1 KB aligned), the peer's
-// partial logits and the record list.
-constexpr size_t kKv4Head = 3 * 1024;
+constexpr size_t kKv4Head = 8 * 1024;
 static_assert(sizeof(Kv4Smem) <= kKv4Head, "the head holds the barriers");
-constexpr size_t kKv4SmemBytes = kKv4Head + kAttnStages * kAttnStage + 2 * kAttnHeads * kAttnTileN * 4 + kKv4MaxK * 4;
+constexpr size_t kKv4SmemBytes = kKv4Head + 3 * kKv4QPanel + kKv4Kx + 3 * kKv4V + 2 * kKv4P;
 static_assert(kKv4SmemBytes <= 232448, "dynamic shared memory of one CTA");
-static_assert(2 * kKv4MaxK * 4 <= kAttnStages * kAttnStage, "the selection's table fits the stages");
-
-// A record's part of one tile row and panel: 64 codes, their four scale codes,
-// and 8 positional features.
-struct Kv4Piece {
-  uint32_t w[8];
-  uint32_t scales;
-  uint4 rope;
-};
-
-__device__ __forceinline__ void kv4_load_piece(Kv4Piece& k, const uint8_t* rec, uint32_t rank, int panel) {
-  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(k.w[0]), "=r"(k.w[1]), "=r"(k.w[2]), "=r"(k.w[3]), "=r"(k.w[4]), "=r"(k.w[5]), "=r"(k.w[6]),
-                 "=r"(k.w[7])
-               : "l"(rec + rank * 128 + panel * 32));
-  k.scales = __ldg(reinterpret_cast<const uint32_t*>(rec + kKv4ScaleAt + rank * 16 + panel * 4));
-  k.rope = __ldg(reinterpret_cast<const uint4*>(rec + kKv4RopeAt + rank * 64 + panel * 16));
-}
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// One lane of a converged warp, in a way the compiler can see: the branch it
+// takes runs on the uniform datapath.  An MMA issued behind `lane == 0` costs
+// its thread 45 cycles (80 beside other warps), behind this one 32, the rate of
+// an M = 128, N = 64 bf16 MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
+// Arrive on a barrier of another CTA of the cluster (a cluster address).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// 16 bytes into shared memory on their own, zeros unless `valid`.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void stg256(void* dst, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Two bf16 times f, each rounded once.
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t x, float f) {
+  return pack_bf16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
+}
+
+// Arrive once on `bar` of CTA `rank` of the cluster (the same place in its
+// shared memory) when all previously issued tcgen05 operations of this thread
+// have completed.
+__device__ __forceinline__ void mma_commit_to(uint64_t* bar, uint32_t rank) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          sm100::smem_u32(bar)),
+      "h"(static_cast<uint16_t>(1u << rank))
+      : "memory");
+}
+
+__device__ __forceinline__ void st_async_b32(uint32_t addr, float v, uint32_t remote_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(__float_as_uint(v)), "r"(remote_bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_async_v4u(uint32_t addr, const uint32_t (&v)[4], uint32_t remote_bar) {
+  sm100::st_async_v4(addr, __uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]),
+                     remote_bar);
+}
+
+// Shared-memory descriptor of a K-major operand without swizzle, stored as
+// [16-byte piece of a row][row][16 B]: 8 rows of one piece are a 128-byte core
+// matrix, the next 8 rows 128 bytes on, the next piece (8 bf16 of K) `lbo` on.
+__device__ __forceinline__ uint64_t desc_k_none(uint32_t smem_addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// ---------------------------------------------------------------- work items
+
+// A work item, one (query, head slice, part): its tiles are t = 0 .. tiles-1,
+// those with t & 1 == rank are this CTA's own.  The part's keys are list[first
+// .. first + n).
+struct Kv4Item {
+  int64_t row;               // within this launch
+  int slice, part, tiles, first, n;
+  __device__ __forceinline__ Kv4Item(const Kv4AttnParams& p, int64_t item) {
+    part = static_cast<int>(item % p.parts);
+    slice = static_cast<int>(item / p.parts % p.slices);
+    row = item / p.parts / p.slices;
+    const int n_row = __ldg(p.count + row);
+    const int t_row = (n_row + kAttnTileN - 1) / kAttnTileN;
+    const int t0 = static_cast<int>(static_cast<int64_t>(t_row) * part / p.parts);
+    tiles = static_cast<int>(static_cast<int64_t>(t_row) * (part + 1) / p.parts) - t0;
+    first = t0 * kAttnTileN;
+    n = min(n_row - first, tiles * kAttnTileN);
+  }
+  __device__ __forceinline__ int own(uint32_t rank) const { return (tiles + 1 - static_cast<int>(rank)) >> 1; }
+  __device__ __forceinline__ int keys_of(int t) const { return min(kAttnTileN, n - t * kAttnTileN); }
+};
+
+// Half of a record's codes for one tile row and panel (64 codes and their four
+// scale codes) as bf16 into 128 swizzled bytes of a panel row.
+struct Kv4Piece {
+  uint32_t w[8];
+  uint32_t scales;
+};
+
+__device__ __forceinline__ void ldg256(uint32_t (&w)[8], const uint8_t* src) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(src));
+}
+
+// A load that stays where it is written: the compiler moves plain ones down to
+// their use, and the latency with them.
+__device__ __forceinline__ uint32_t ldg32_here(const void* src) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(src));
+  return v;
+}
+
+__device__ __forceinline__ void kv4_load_piece(Kv4Piece& k, const uint8_t* rec, int panel) {
+  ldg256(k.w, rec + panel * 32);
+  k.scales = ldg32_here(rec + kKv4ScaleAt + panel * 4);
+}
+
+__device__ __forceinline__ const uint8_t* kv4_at(const Kv4AttnParams& p, uint32_t id) {
+  return p.cache + static_cast<int64_t>(id) * kKv4Record;
+}
+
+// To the 128 bytes at `row_at` (row r of a panel), piece c at place c ^ (r & 7),
+// in the order c ^ 2 panel: the codes' 16-feature groups, two words each, change
+// places by the bits of `panel` instead of being indexed by it.
+__device__ __forceinline__ void kv4_store_piece(const Kv4Piece& k, uint32_t row_at, int r, int panel) {
+  const uint32_t at = row_at | (((r & 7) ^ (2 * panel)) << 4);
+  const bool p0 = panel & 1, p1 = panel & 2;
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = p0 ? k.w[i ^ 2] : k.w[i], b = p0 ? k.w[i ^ 6] : k.w[i ^ 4];
+    w[i] = p1 ? b : a;
+  }
+  const uint32_t scales = __byte_perm(k.scales, 0u, 0x3210u ^ (0x1111u * panel));
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint32_t s16, m24, d[4];
+    kv4_scales(scales, g, s16, m24);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      kv4_decode8(w[2 * g + u], s16, m24, d);
+      sts128(at ^ ((2 * g + u) << 4), d[0], d[1], d[2], d[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
 __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnParams p) {
   using namespace sm100;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Kv4Smem* sm = reinterpret_cast<Kv4Smem*>(smem_raw);
-  uint8_t* kv_buf = smem_raw + kKv4Head;
-  float* x_buf = reinterpret_cast<float*>(kv_buf + kAttnStages * kAttnStage);   // [2 parities][16 pieces][128 rows][4]
-  int32_t* list = reinterpret_cast<int32_t*>(x_buf + 2 * kAttnHeads * kAttnTileN);
+  uint8_t* q_buf = smem_raw + kKv4Head;                  // [3 panels][128 rows][128 B], swizzled
+  uint8_t* kx_buf = q_buf + 3 * kKv4QPanel;              // [4 latent panels of the other half, positional][64 rows][128 B]
+  uint8_t* vo_buf = kx_buf + kKv4Kx;                     // [2 own tiles][4 panels][64 rows][128 B]
+  uint8_t* vr_buf = vo_buf + 2 * kKv4V;                  // [4 panels][64 rows][128 B]
+  uint8_t* p_own = vr_buf + kKv4V;                       // [8 pieces][128 rows][16 B]
+  uint8_t* p_peer = p_own + kKv4P;
   volatile int* abort_flag = &sm->abort_flag;
   if (smem_u32(smem_raw) & 1023u) {                      // the swizzles need it; the same in every CTA
     if (threadIdx.x == 0) record_status(HISA_ERR_UNSUPPORTED);
@@ -214,332 +414,517 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
-  const int64_t item = cluster_id_x();                   // (row, head slice, part)
-  const int part = static_cast<int>(item % p.parts);
-  const int slice = static_cast<int>(item / p.parts % p.slices);
-  const int64_t row = item / p.parts / p.slices;
+  const int64_t item0 = cluster_id_x(), step = gridDim.x / 2;
+  // bytes that the peer's softmax sends with a tile (weights, references, the
+  // warps' marks) and with a query (sums and references)
+  constexpr uint32_t kPBytes = kKv4P + 2 * kAttnHeads * 4 + 8 * 4, kFinBytes = 4 * kAttnHeads * 4;
 
   if (tid == 0) {
-    mbar_init(&sm->q_full, 256);
-    for (int i = 0; i < kAttnStages; ++i) {
-      mbar_init(&sm->kv_full[i], kKv4ProdWarps);
-      mbar_init(&sm->kv_empty[i], 1);
+    mbar_init(&sm->q_full, 4);
+    mbar_init(&sm->q_free, 1);
+    mbar_init(&sm->o_empty, 4);
+    mbar_init(&sm->kx_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->vo_full[i], 4);
+      mbar_init(&sm->vo_empty[i], 1);
+      // rank 1: a local arrive announcing the bytes + the peer's st.async; rank 0: the writing group's warps
+      mbar_init(&sm->first_full[i], rank == 0 ? 4 : 1);
+      mbar_init(&sm->drain[i], 1);
     }
+    mbar_init(&sm->vr_full, 4);
+    mbar_init(&sm->vr_empty, 1);
     mbar_init(&sm->s_full, 1);
-    mbar_init(&sm->s_empty, 256);
-    mbar_init(&sm->p_full, 256);
-    mbar_init(&sm->pv_done, 1);
-    for (int i = 0; i < 2; ++i)
-      for (int hf = 0; hf < 2; ++hf)
-        mbar_init(&sm->x_full[i][hf], 1);   // local arrive with a half tile's bytes + the peer's st.async bytes
-    for (int i = 0; i < 4; ++i) mbar_init(&sm->pair[i], 2);
-    mbar_init(&sm->drain[0], 1);
-    mbar_init(&sm->drain[1], 1);
+    mbar_init(&sm->s_empty, 8);
+    mbar_init(&sm->p_own, 8);
+    mbar_init(&sm->p_peer, 1);                   // announced bytes + the peer's st.async
+    mbar_init(&sm->p_free, 2);                   // the output MMAs of both CTAs
+    mbar_init(&sm->ctl, 1);
+    mbar_init(&sm->fix_done, 4);
+    for (int i = 0; i < 16; ++i) sm->moved[i >> 3][i & 7] = 0;
+    mbar_init(&sm->fin_own, 8);
+    mbar_init(&sm->fin_peer, 1);                 // announced bytes
+    mbar_init(&sm->fin_free, 8);                 // the output warps of both CTAs
     sm->abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(&sm->tmem_base, 512);
-  const int n = kv4_select<kKv4Threads>(p, row, list, reinterpret_cast<uint32_t*>(kv_buf), p.slots, sm->scan);
-  // the selection's table lies where the producers store keys for the tensor
-  // cores: those stores are generic too and fenced before each hand-over
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                      // the peer's barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
-  // this part's run of the row's tiles
-  const int T_row = (n + kAttnTileN - 1) / kAttnTileN;
-  const int t0 = static_cast<int>(static_cast<int64_t>(T_row) * part / p.parts);
-  const int T = static_cast<int>(static_cast<int64_t>(T_row) * (part + 1) / p.parts) - t0;
-  const int first = t0 * kAttnTileN;                   // this part's first key in the list
-  const int n_part = min(n - first, T * kAttnTileN);
+  auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {    // by all lanes, the outcome warp-uniform
+    return __all_sync(kFull, mbar_wait(bar, phase & 1, abort_flag));
+  };
+  auto wait_peer = [&](uint64_t* bar, uint32_t phase) -> bool {   // completed by the other CTA
+    return __all_sync(kFull, mbar_wait_cluster(bar, phase & 1, abort_flag));
+  };
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ logit MMA issuer
-    // S = q_c . k_c^T for tile k as soon as its keys are in shared memory and
-    // the softmax has read tile k-1 out of the single logit buffer; the output
-    // MMAs come from another thread, so these never queue behind them
-    if (lane == 0) {
+    // S = q . k^T of own tile u, once its keys are in shared memory and the
+    // softmax has read tile u-1 out of the single logit buffer
+    if (elect_one()) {
       constexpr uint32_t id_qk = instr_desc(kAttnHeads, kAttnTileN, 1u);
-      bool ok = T == 0 || mbar_wait(&sm->q_full, 0, abort_flag);
-      if (ok) tc_fence_after();
-      for (int k = 0; ok && k < T; ++k) {
-        const int st = k % kAttnStages;
-        if (!(ok = mbar_wait(&sm->kv_full[st], static_cast<uint32_t>((k / kAttnStages) & 1), abort_flag))) break;
-        if (k >= 1 && !(ok = mbar_wait(&sm->s_empty, static_cast<uint32_t>((k - 1) & 1), abort_flag))) break;
+      const uint64_t q_desc = desc_k_sw128(smem_u32(q_buf)), kx_desc = desc_k_sw128(smem_u32(kx_buf));
+      uint32_t u = 0, live = 0;
+      bool ok = true;
+      for (int64_t item = item0; ok && item < p.items; item += step) {
+        const int own = Kv4Item(p, item).own(rank);
+        if (own == 0) continue;
+        if (!(ok = mbar_wait(&sm->q_full, live & 1, abort_flag))) break;
+        ++live;
         tc_fence_after();
-        const uint32_t base = smem_u32(kv_buf + st * kAttnStage);
-        const uint64_t k_desc = desc_k_sw128(base);
+        for (int k = 0; k < own; ++k, ++u) {
+          const uint64_t vo_desc = desc_k_sw128(smem_u32(vo_buf + (u & 1) * kKv4V));
+          if (!(ok = mbar_wait(&sm->vo_full[u & 1], (u >> 1) & 1, abort_flag))) break;
+          if (u >= 1 && !(ok = mbar_wait(&sm->s_empty, (u - 1) & 1, abort_flag))) break;
+          tc_fence_after();
+          // the value half's four panels, which are there early; meanwhile
+          // the rest of the row is made: the other half's four and the
+          // positional one, whose single buffer the logits before have freed
 #pragma unroll
-        for (int ks = 0; ks < 4 * kAttnPanels; ++ks)
-          mma_ts(tmem + kAttnTmemS, tmem + kAttnTmemQ + ks * 8,
-                 k_desc + static_cast<uint64_t>((ks >> 2) * (kAttnPanelK / 16) + (ks & 3) * 2), id_qk, ks > 0 ? 1u : 0u);
-        const uint64_t r_desc = desc_k_sw64(base + kAttnPanels * kAttnPanelK);
+          for (int pn = 0; pn < 9; ++pn) {
+            if (pn == 4 && !(ok = mbar_wait(&sm->kx_full, u & 1, abort_flag))) break;
+            const uint32_t panel = pn < 4 ? 4 * rank + pn : pn < 8 ? 4 * peer + pn - 4 : 8u;    // of the row
+            const uint64_t kd = pn < 4 ? vo_desc + static_cast<uint64_t>(pn * (kKv4Panel / 16))
+                                       : kx_desc + static_cast<uint64_t>((pn - 4) * (kKv4Panel / 16));
+            if (panel < kKv4QPanels) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-          mma_ts(tmem + kAttnTmemS, tmem + kAttnTmemQ + (4 * kAttnPanels + ks) * 8, r_desc + static_cast<uint64_t>(ks * 2),
-                 id_qk, 1u);
-        mma_commit(&sm->s_full);
+              for (int ks = 0; ks < 4; ++ks)
+                mma_ts(tmem + kKv4TmemS, tmem + kKv4TmemQ + panel * 32 + ks * 8, kd + static_cast<uint64_t>(ks * 2),
+                       id_qk, (pn > 0 || ks > 0) ? 1u : 0u);
+            } else {
+              const uint64_t qd = q_desc + static_cast<uint64_t>((panel - kKv4QPanels) * (kKv4QPanel / 16));
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma<DT_BF16>(tmem + kKv4TmemS, qd + static_cast<uint64_t>(ks * 2), kd + static_cast<uint64_t>(ks * 2),
+                             id_qk, (pn > 0 || ks > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          mma_commit(&sm->s_full);
+        }
+        if (ok) mma_commit(&sm->q_free);
       }
       mma_commit(&sm->drain[0]);
       mbar_drain(&sm->drain[0], 0);
     }
-  } else if (warp == kAttnPvWarp) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ output MMA issuer
-    // O_c += P . V_c for tile j once the softmax has written P_j; the tile's
-    // key stage is free when this MMA completes
-    if (lane == 0) {
+    // O_r += P . V_r, every tile in turn; where a softmax warp has moved a
+    // reference the output warps first bring output and weights to one
+    if (elect_one()) {
       constexpr uint32_t id_pv = instr_desc_bmn(kAttnHeads, 256);
+      uint32_t u = 0, v = 0, live = 0, fixes = 0, drains = 0;
       bool ok = true;
-      for (int j = 0; ok && j < T; ++j) {
-        const int sj = j % kAttnStages;
-        if (!(ok = mbar_wait(&sm->p_full, static_cast<uint32_t>(j & 1), abort_flag))) break;
-        tc_fence_after();
-        // V: the four 64-feature value panels of the key tile, MN-major
-        const uint32_t v0 = smem_u32(kv_buf + sj * kAttnStage);
+      mbar_arrive_expect_tx(&sm->p_peer, kPBytes);     // the first of the peer's weights
+      for (int64_t item = item0; ok && item < p.items; item += step) {
+        const int tiles = Kv4Item(p, item).tiles;
+        if (tiles == 0) continue;
+        // the previous query's output has been read
+        if (live > 0 && !(ok = mbar_wait(&sm->o_empty, (live - 1) & 1, abort_flag))) break;
+        ++live;
+        for (int t = 0; t < tiles; ++t) {
+          const bool mine = (t & 1u) == rank;
+          if (!(ok = mine ? mbar_wait(&sm->p_own, u & 1, abort_flag)
+                          : mbar_wait_cluster(&sm->p_peer, v & 1, abort_flag) && mbar_wait(&sm->vr_full, v & 1, abort_flag)))
+            break;
+          const uint4 m0 = lds128(smem_u32(sm->moved[mine ? 0 : 1])), m1 = lds128(smem_u32(sm->moved[mine ? 0 : 1] + 4));
+          const uint32_t tag = (mine ? u : v) + 1;
+          if (m0.x == tag || m0.y == tag || m0.z == tag || m0.w == tag || m1.x == tag || m1.y == tag || m1.z == tag ||
+              m1.w == tag) {
+            mma_commit(&sm->drain[1]);                 // every MMA before
+            if (!(ok = mbar_wait(&sm->drain[1], drains++ & 1, abort_flag))) break;
+            sm->command = kKv4Scale + (t == 0 ? kKv4First : 0) + (mine ? 0 : kKv4Peer);
+            mbar_arrive(&sm->ctl);
+            if (!(ok = mbar_wait(&sm->fix_done, fixes++ & 1, abort_flag))) break;
+          }
+          if (!mine) {
+            mbar_arrive_expect_tx(&sm->p_peer, kPBytes);
+            fence_proxy_async_smem();                  // the peer's generic-proxy writes before the MMA's reads
+          }
+          tc_fence_after();
+          // V: the four 64-feature value panels of the key tile, MN-major
+          const uint64_t v_desc =
+              desc_mn_sw128(smem_u32(mine ? vo_buf + (u & 1) * kKv4V : vr_buf), kKv4Panel, 1024);
+          const uint64_t p_desc = desc_k_none(smem_u32(mine ? p_own : p_peer), kAttnHeads * 16);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint64_t vd = desc_mn_sw128(v0 + ks * 16 * 128, kAttnPanelK, 1024);
-          mma_ts(tmem + kAttnTmemO, tmem + kAttnTmemP + ks * 8, vd, id_pv, (j > 0 || ks > 0) ? 1u : 0u);
+          for (int ks = 0; ks < 4; ++ks)
+            mma<DT_BF16>(tmem + kKv4TmemO, p_desc + static_cast<uint64_t>(ks * (2 * kAttnHeads * 16 / 16)),
+                         v_desc + static_cast<uint64_t>(ks * (16 * 128 / 16)), id_pv, (t > 0 || ks > 0) ? 1u : 0u);
+          mma_commit(mine ? &sm->vo_empty[u & 1] : &sm->vr_empty);
+          if (mine) {
+            mma_commit(&sm->p_free);
+            ++u;
+          } else {
+            mma_commit_to(&sm->p_free, peer);
+            ++v;
+          }
         }
-        mma_commit(&sm->kv_empty[sj]);
-        mma_commit(&sm->pv_done);
+        if (!ok) break;
+        mma_commit(&sm->drain[1]);
+        if (!(ok = mbar_wait(&sm->drain[1], drains++ & 1, abort_flag))) break;
+        sm->command = kKv4Done;
+        mbar_arrive(&sm->ctl);
       }
       mma_commit(&sm->drain[1]);
-      mbar_drain(&sm->drain[1], 0);
+      mbar_drain(&sm->drain[1], drains & 1);
     }
   } else if (warp < kKv4SoftBase / 32) {
     // ------------------------------------------------------------ key producers
-    // Lane l has row 8w + (l & 7) and panel l >> 3 of every tile: four lanes
-    // read a row's 128 consecutive code bytes, and the eight lanes of a store
-    // phase hit eight rows of one panel, which the swizzle keeps in distinct
-    // banks.  The next tile's record is on its way while this one is turned.
-    const int r = (warp - kKv4ProdBase / 32) * 8 + (lane & 7);
-    const int panel = lane >> 3;
-    auto load = [&](Kv4Piece& k, int tile) {
-      // past the last key: that key again, masked by the softmax
-      const int e = min(tile * kAttnTileN + r, n_part - 1);
-      kv4_load_piece(k, p.cache + static_cast<int64_t>(list[first + e]) * kKv4Record, rank, panel);
-    };
-    const uint32_t row_at = smem_u32(kv_buf) + panel * kAttnPanelK + r * 128;
-    const uint32_t rope_at = smem_u32(kv_buf) + kAttnPanels * kAttnPanelK + r * 64 + ((panel ^ ((r >> 1) & 3)) << 4);
-    Kv4Piece cur, nxt;
-    if (T > 0) load(cur, 0);
-    for (int i = 0; i < T; ++i) {
-      const int st = i % kAttnStages;
-      if (i + 1 < T) load(nxt, i + 1);
-      int okl = 1;
-      if (lane == 0)
-        okl = mbar_wait(&sm->kv_empty[st], static_cast<uint32_t>(((i / kAttnStages) & 1) ^ 1), abort_flag);
-      if (__shfl_sync(kFull, okl, 0) == 0) break;
+    // Lane l has panel l & 3 and a row with r & 7 = l >> 2: four lanes read a
+    // row's 128 consecutive code bytes (lanes of a row further apart would
+    // take a pass of the load pipe each).  The eight lanes of a store phase
+    // are two rows of four panels, whose places differ only in r & 1 for the
+    // same piece; so a lane takes its pieces in the order c ^ 2 panel.
+    // Registers are loaded again, for the next tile, as soon as they are
+    // stored, with record numbers looked up one tile before that.
+    // One code for the three teams (three copies of it, and instruction
+    // fetches hold up every warp).
+    const int pw = warp - kKv4ProdBase / 32, team = pw >> 2;     // 0: query, peer's values; 1: own values; 2: own rest
+    const int panel = lane & 3;
+    const int r = (pw & 3) * 16 + (lane >> 2);         // and r + 8
+    const uint32_t kind = team == 0 ? peer : rank;     // parity of the team's tiles
+    const uint32_t code_panel = 4 * (team == 2 ? peer : rank) + panel;     // of a record
+    const uint32_t out_at = smem_u32(team == 0 ? vr_buf : team == 1 ? vo_buf : kx_buf) + panel * kKv4Panel + r * 128;
+    const uint32_t rope_at = smem_u32(kx_buf) + 4 * kKv4Panel + ((r * 128) | (((2 * panel) ^ (r & 7)) << 4));
+    uint32_t n = 0, loaded = 0;                        // tiles made, queries loaded, through all queries
+    bool ok = true;
+    for (int64_t item = item0; ok && item < p.items; item += step) {
+      const Kv4Item it(p, item);
+      if (team == 0 && it.own(rank) > 0) {
+        // the query's rows, behind the last own logits of the one before:
+        // three panels at a time into shared memory (eight lanes a row: a line
+        // a row and panel), the first six from there into TMEM
+        const int quarter = warp & 3, h = quarter * 32 + lane;
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint16_t* qs = p.q + ((p.row0 + it.row) * p.heads + it.slice * kAttnHeads) * kAttnDqk;
+        const int heads = min(kAttnHeads, p.heads - it.slice * kAttnHeads);
+        if (h < heads)                                 // towards L2 until then
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t s16, m24, d[4];
-        kv4_scales((cur.scales >> (8 * g)) & 255u, s16, m24);
+          for (int i = 0; i < 9; ++i) prefetch_l2(qs + h * kAttnDqk + 64 * i);
+        if (loaded > 0 && !(ok = wait(&sm->q_free, loaded - 1))) break;
+        ++loaded;
+        tc_fence_after();
+#pragma unroll 1
+        for (int p0 = 0; p0 < 9; p0 += 3) {
+          // a warp's rows are its own: no other warp reads or writes them
+#pragma unroll 1
+          for (int pn = 0; pn < 3; ++pn) {
+#pragma unroll 2
+            for (int i = 0; i < 8; ++i) {
+              const int hr = quarter * 32 + i * 4 + (lane >> 3), c = lane & 7;
+              const bool ok_row = hr < heads;
+              cp_async16(smem_u32(q_buf) + pn * kKv4QPanel + hr * 128 + ((c ^ (hr & 7)) << 4),
+                         qs + (ok_row ? hr : 0) * kAttnDqk + (p0 + pn) * 64 + c * 8, ok_row);
+            }
+          }
+          cp_async_wait_all();
+          __syncwarp();
+          if (p0 + 3 > kKv4QPanels) break;
+#pragma unroll 1
+          for (int pn = 0; pn < 6; ++pn) {             // half panels
+            uint32_t x[16];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          kv4_decode8(cur.w[2 * g + u], s16, m24, d);
-          sts128(row_at + st * kAttnStage + (((2 * g + u) ^ (r & 7)) << 4), d[0], d[1], d[2], d[3]);
+            for (int i = 0; i < 4; ++i) {
+              const uint4 y = lds128(smem_u32(q_buf) + (pn >> 1) * kKv4QPanel + h * 128 + ((((pn & 1) * 4 + i) ^ (h & 7)) << 4));
+              x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+            }
+            tmem_st16(t_lane + kKv4TmemQ + p0 * 32 + pn * 16, x);
+          }
+          __syncwarp();
         }
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        warp_arrive(&sm->q_full);
       }
-      sts128(rope_at + st * kAttnStage, cur.rope.x, cur.rope.y, cur.rope.z, cur.rope.w);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->kv_full[st]);
-      cur = nxt;
+      const int mine = it.own(kind);
+      if (mine == 0) continue;
+      const int32_t* list = p.list + it.row * p.list_ld + it.first;
+      // the record of the tile's row rr; past the last key that key's again, masked by the softmax
+      int row0 = static_cast<int>(kind) * kAttnTileN + r;
+      auto record = [&](int rr) -> uint32_t { return ldg32_here(list + min(row0 + rr, it.n - 1)); };
+      Kv4Piece a, b;
+      uint32_t ra[8], rb[8];                           // team 2: 16 of each row's 64 positional features
+      uint32_t ida = record(0), idb = record(8);
+#pragma unroll 1
+      for (int i = -1; i < mine; ++i) {
+        if (i >= 0) {
+          uint32_t at = out_at;
+          uint64_t* full;
+          if (team == 0) {
+            if (n >= 1 && !(ok = wait(&sm->vr_empty, n - 1))) break;
+            full = &sm->vr_full;
+          } else if (team == 1) {
+            if (n >= 2 && !(ok = wait(&sm->vo_empty[n & 1], (n >> 1) - 1))) break;
+            at += (n & 1) * kKv4V;
+            full = &sm->vo_full[n & 1];
+          } else {
+            if (n >= 1 && !(ok = wait(&sm->s_full, n - 1))) break;     // the logits of the own tile before are done
+            full = &sm->kx_full;
+            sts128(rope_at, ra[0], ra[1], ra[2], ra[3]);
+            sts128(rope_at ^ 16u, ra[4], ra[5], ra[6], ra[7]);
+            sts128(rope_at + 8 * 128, rb[0], rb[1], rb[2], rb[3]);
+            sts128((rope_at + 8 * 128) ^ 16u, rb[4], rb[5], rb[6], rb[7]);
+          }
+          kv4_store_piece(a, at, r, panel);
+          kv4_store_piece(b, at + 8 * 128, r, panel);
+          fence_proxy_async_smem();
+          warp_arrive(full);
+          ++n;
+        }
+        // the addresses not before here: they wait for the record numbers
+        asm volatile("" : "+r"(ida), "+r"(idb));
+        const uint8_t *pa = kv4_at(p, ida), *pb = kv4_at(p, idb);
+        kv4_load_piece(a, pa, code_panel);
+        kv4_load_piece(b, pb, code_panel);
+        if (team == 2) {
+          ldg256(ra, pa + kKv4RopeAt + panel * 32);
+          ldg256(rb, pb + kKv4RopeAt + panel * 32);
+        }
+        row0 += 2 * kAttnTileN;
+        ida = record(0);
+        idb = record(8);
+      }
     }
-  } else {
-    // ------------------------------------------------------------ softmax
+  } else if (warp < kKv4CorrBase / 32) {
+    // ------------------------------------------------------------ softmax of the own tiles
     const int quarter = warp & 3, g = (warp - kKv4SoftBase / 32) >> 2;
     const int h = quarter * 32 + lane;                 // head row = TMEM lane
-    const bool head_ok = slice * kAttnHeads + h < p.heads;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    constexpr uint32_t kXBytes = kAttnHeads * kAttnTileN * 4;           // one exchange buffer
-    const uint32_t peer_x = peer_addr(x_buf + (8 * g * kAttnHeads + h) * 4, peer);   // + buffer * kXBytes + piece * 2 KB
-    const uint32_t peer_x_full = peer_addr(&sm->x_full[0][g], peer);    // + buffer * 16
+    const uint32_t p_off = 4 * g * (kAttnHeads * 16) + h * 16;      // + piece (8 keys) * 2 KB
+    const uint32_t p_at = smem_u32(p_own) + p_off;
+    const uint32_t peer_p = peer_addr(p_peer + p_off, peer), peer_p_bar = peer_addr(&sm->p_peer, peer);
+    const uint32_t peer_m = peer_addr(&sm->m_peer[g][h], peer);
+    const uint32_t peer_mark = peer_addr(&sm->moved[1][warp - kKv4SoftBase / 32], peer);
     const float kInf = __int_as_float(0x7f800000);
-    float m = -kInf, l = 0.f;
+    uint32_t u = 0, live = 0;
+    uint32_t first_phase[2] = {0, 0};
     bool ok = true;
-    if (T > 0) {
-      // this head's part of the query into TMEM: group g has value panels 2g
-      // and 2g+1, group 0 the 32 positional features too
-      const uint4* qh = reinterpret_cast<const uint4*>(p.q + ((row * p.heads) + slice * kAttnHeads + (head_ok ? h : 0)) *
-                                                                 static_cast<int64_t>(kAttnDqk));
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 1
-      for (int pn = 2 * g; pn < 2 * g + 2; ++pn) {
-        uint32_t v[32];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint4 x = head_ok ? __ldg(qh + rank * 32 + pn * 8 + u) : zero;
-          v[4 * u] = (x.x & p.q_keep) ^ p.q_flip;
-          v[4 * u + 1] = (x.y & p.q_keep) ^ p.q_flip;
-          v[4 * u + 2] = (x.z & p.q_keep) ^ p.q_flip;
-          v[4 * u + 3] = (x.w & p.q_keep) ^ p.q_flip;
-        }
-        tmem_st32(t_lane + kAttnTmemQ + pn * 32, v);
-      }
-      if (g == 0) {
-        uint32_t v[16];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint4 x = head_ok ? __ldg(qh + kAttnDv / 8 + rank * 4 + u) : zero;
-          v[4 * u] = (x.x & p.q_keep) ^ p.q_flip;
-          v[4 * u + 1] = (x.y & p.q_keep) ^ p.q_flip;
-          v[4 * u + 2] = (x.z & p.q_keep) ^ p.q_flip;
-          v[4 * u + 3] = (x.w & p.q_keep) ^ p.q_flip;
-        }
-        tmem_st16(t_lane + kAttnTmemQ + 32 * kAttnPanels, v);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&sm->q_full);
-    }
-    // Every wait below is taken by all lanes and its outcome made
-    // warp-uniform: the tcgen05 loads and stores that follow are .sync.aligned.
-    //
-    // The exchange of partial logits is sparse_attn.cuh's, each group with its
-    // key half and barrier: a buffer is written again two tiles later, when
-    // the peer's group has received all of my group's next tile, which each
-    // of my threads sends after reading its row of this one.
-    auto load_send = [&](float (&dst)[32], int tile) -> bool {
-      if (!__all_sync(kFull, mbar_wait(&sm->s_full, static_cast<uint32_t>(tile & 1), abort_flag))) return false;
-      tc_fence_after();
-      uint32_t v[32];
-      tmem_ld32(t_lane + kAttnTmemS + 32 * g, v);
-      tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < 32; ++j) dst[j] = __uint_as_float(v[j]);
-      tc_fence_before();
-      mbar_arrive(&sm->s_empty);
-      const int xb = tile & 1;
-      if (h == 0) mbar_arrive_expect_tx(&sm->x_full[xb][g], kXBytes / 2);
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        st_async_v4(peer_x + xb * kXBytes + c * (kAttnHeads * 16), dst[4 * c], dst[4 * c + 1], dst[4 * c + 2],
-                    dst[4 * c + 3], peer_x_full + xb * 16);
-      return true;
-    };
-    // The other group's value for this row; `turn` counts the exchanges.
-    auto swap_pair = [&](float v, int turn, float& other) -> bool {
-      sm->red[turn & 1][g][h] = v;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->pair[quarter]);
-      if (!__all_sync(kFull, mbar_wait(&sm->pair[quarter], static_cast<uint32_t>(turn & 1), abort_flag))) return false;
-      other = sm->red[turn & 1][g ^ 1][h];
-      return true;
-    };
-    float s[32], sn[32];
-    if (T > 0) ok = load_send(s, 0);
-    for (int i = 0; ok && i < T; ++i) {
-      // 1. the peer's part of tile i, sent one tile ago
-      const int xb = i & 1;
-      if (!(ok = __all_sync(kFull, mbar_wait_cluster(&sm->x_full[xb][g], static_cast<uint32_t>((i >> 1) & 1),
-                                                     abort_flag))))
-        break;
-      const float4* x4 = reinterpret_cast<const float4*>(x_buf + xb * (kAttnHeads * kAttnTileN)) + 8 * g * kAttnHeads + h;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float4 v = x4[c * kAttnHeads];
-        s[4 * c + 0] += v.x; s[4 * c + 1] += v.y; s[4 * c + 2] += v.z; s[4 * c + 3] += v.w;
-      }
-      // 2. my part of tile i+1 out to the peer
-      if (i + 1 < T && !(ok = load_send(sn, i + 1))) break;
-      // 3. online softmax of tile i in the log2 domain, with the reference
-      // that moves only when the maximum exceeds it by 8 (sparse_attn.cuh)
-      const int nk = n_part - i * kAttnTileN - 32 * g;   // this group's keys of the tile
-      if (nk < 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) s[j] = j < nk ? s[j] : -kInf;
-      }
-      float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
-      float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])), mo;
-      if (!(ok = swap_pair(mt, i, mo))) break;
-      mt = fmaxf(mt, mo) * p.scale_log2;
-      const bool move = i == 0 || mt > m + 8.f;
-      const float mx = move ? mt : m;
-      const float corr = (i == 0) ? 0.f : (move ? fast_exp2(m - mx) : 1.f);
-      float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        s[j] = fast_exp2(__fmaf_rn(s[j], p.scale_log2, -mx));
-        sum4[j & 3] += s[j];
-      }
-      l = l * corr + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-      m = mx;
-      // P and O belong to the previous tile's output MMA until it completes
-      if (i >= 1 &&
-          !(ok = __all_sync(kFull, mbar_wait(&sm->pv_done, static_cast<uint32_t>((i - 1) & 1), abort_flag))))
-        break;
-      tc_fence_after();
-      {
-        uint32_t v[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-        tmem_st16(t_lane + kAttnTmemP + 16 * g, v);
-      }
-      if (i >= 1 && __any_sync(kFull, corr != 1.f)) {    // rows whose maximum did not grow scale by 1
-#pragma unroll 1
-        for (int c0 = 128 * g; c0 < 128 * g + 128; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(t_lane + kAttnTmemO + c0, v);
+    for (int64_t item = item0; ok && item < p.items; item += step) {
+      const Kv4Item it(p, item);
+      if (it.tiles == 0) continue;
+      const int own = it.own(rank);
+      const uint32_t par = live & 1;
+      if (rank == 1 && own > 0 && g == 0 && h == 0) mbar_arrive_expect_tx(&sm->first_full[par], kAttnHeads * 4);
+      float m = -kInf, m_first = 0.f, l = 0.f;
+      for (int k = 0; k < own; ++k, ++u) {
+        if (!(ok = wait(&sm->s_full, u))) break;
+        tc_fence_after();
+        float s[32];
+        {
+          uint32_t x[32];
+          tmem_ld32(t_lane + kKv4TmemS + 32 * g, x);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * corr);
-          tmem_st32(t_lane + kAttnTmemO + c0, v);
+          for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(x[i]);
         }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&sm->p_full);
+        tc_fence_before();
+        warp_arrive(&sm->s_empty);
+        if (p.sign != 1) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s[j] = sn[j];
+          for (int i = 0; i < 32; ++i) s[i] = p.sign == 0 ? 0.f : -s[i];
+        }
+        const int nk = it.keys_of(2 * k + static_cast<int>(rank)) - 32 * g;
+        if (nk < 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = i < nk ? s[i] : -kInf;
+        }
+        float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
+        const float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+        // the reference: the maximum of the query's first 32 keys, handed to
+        // the other group and both of the peer's; it stays unless exceeded by 2^64
+        if (k == 0) {
+          if (rank == 0 && g == 0) {
+            m_first = mt;
+            if (it.tiles > 1)
+              st_async_b32(peer_addr(&sm->m_first[par][h], peer), mt, peer_addr(&sm->first_full[par], peer));
+            sm->m_first[par][h] = mt;
+            warp_arrive(&sm->first_full[par]);
+          } else {
+            const uint32_t phase = par ? first_phase[1] : first_phase[0];
+            if (!(ok = rank == 0 ? wait(&sm->first_full[par], phase) : wait_peer(&sm->first_full[par], phase))) break;
+            if (par) ++first_phase[1];
+            else ++first_phase[0];
+            m_first = sm->m_first[par][h];
+          }
+          m = m_first;
+        }
+        if (mt > m + 64.f) {
+          l *= fast_exp2(m - mt);
+          m = mt;
+        }
+        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          s[i] = fast_exp2(__fmaf_rn(s[i], p.scale_log2, -m));
+          sum4[i & 3] += s[i];
+        }
+        l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+        // both CTAs' output MMAs have read the weights before
+        if (u >= 1 && !(ok = wait_peer(&sm->p_free, u - 1))) break;
+        const uint32_t mark = __any_sync(kFull, m != m_first) ? u + 1 : 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {                  // 8 keys a piece
+          const uint32_t y[4] = {w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
+          st_async_v4u(peer_p + c * (kAttnHeads * 16), y, peer_p_bar);
+        }
+        st_async_b32(peer_m, m, peer_p_bar);
+        if (lane == 0) {
+          st_async_b32(peer_mark, __uint_as_float(mark), peer_p_bar);
+          sm->moved[0][warp - kKv4SoftBase / 32] = mark;
+        }
+        sm->m_own[g][h] = m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sts128(p_at + c * (kAttnHeads * 16), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();
+        warp_arrive(&sm->p_own);
+      }
+      if (!ok) break;
+      // this group's sums of the query, to both CTAs' output warps
+      if (live > 0 && !(ok = wait_peer(&sm->fin_free, live - 1))) break;
+      const uint32_t fin_bar = peer_addr(&sm->fin_peer, peer);
+      st_async_b32(peer_addr(&sm->fin[1][g][0][h], peer), l, fin_bar);
+      st_async_b32(peer_addr(&sm->fin[1][g][1][h], peer), m, fin_bar);
+      sm->fin[0][g][0][h] = l;
+      sm->fin[0][g][1][h] = m;
+      warp_arrive(&sm->fin_own);
+      ++live;
     }
-    // ---- epilogue: O / l, and lse
-    const int64_t orow = row * p.heads + slice * kAttnHeads + h;
-    const int col0 = static_cast<int>(rank) * 256 + 128 * g;
-    float lo = 0.f;
-    bool have = T > 0 && ok && swap_pair(l, T, lo);
-    have = have && __all_sync(kFull, mbar_wait(&sm->pv_done, static_cast<uint32_t>((T - 1) & 1), abort_flag));
-    if (have) {
+  } else {
+    // ------------------------------------------------------------ output, scaling
+    const int quarter = warp & 3;
+    const int h = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const float kInf = __int_as_float(0x7f800000);
+    const uint32_t peer_fin_free = peer_addr(&sm->fin_free, peer);
+    if (h == 0) mbar_arrive_expect_tx(&sm->fin_peer, kFinBytes);      // the first of the peer's sums
+    uint32_t live = 0, commands = 0;
+
+    bool ok = true;
+    for (int64_t item = item0; ok && item < p.items; item += step) {
+      const Kv4Item it(p, item);
+      const bool head_ok = it.slice * kAttnHeads + h < p.heads;
+      const int64_t orow = it.row * p.heads + it.slice * kAttnHeads + h;      // within this launch
+      uint16_t* out = p.o + (p.row0 * p.heads + orow) * kAttnDv + rank * 256;
+      if (it.tiles == 0) {
+        if (head_ok && p.parts == 1) {
+          const uint32_t zero[8] = {};
+          for (int i = 0; i < 16; ++i) stg256(out + 16 * i, zero);
+        }
+        if (rank == 0 && head_ok) {
+          if (p.parts > 1) p.part_lse[orow * p.parts + it.part] = -kInf;
+          else p.lse[p.row0 * p.heads + orow] = -kInf;
+        }
+        continue;
+      }
+      bool scaled = false;
+      float mo = 0.f;                                  // what the output rows are relative to, once `scaled`
+      while (true) {
+        if (!(ok = wait(&sm->ctl, commands))) break;
+        ++commands;
+        const int command = *reinterpret_cast<volatile int*>(&sm->command);
+        if (command == kKv4Done) break;
+        const bool from_peer = (command & kKv4Peer) != 0;
+        const float ma = from_peer ? sm->m_peer[0][h] : sm->m_own[0][h], mb = from_peer ? sm->m_peer[1][h] : sm->m_own[1][h];
+        const float m = fmaxf(ma, mb);
+        if (command & kKv4First) mo = m;
+        else if (!scaled) mo = sm->m_first[live & 1][h];
+        scaled = true;
+        if (!(command & kKv4First) && __any_sync(kFull, m > mo)) {     // the output moves up to this tile's reference
+          tc_fence_after();
+          const float f = m > mo ? fast_exp2(mo - m) : 1.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 32) {
+            uint32_t x[32];
+            tmem_ld32(t_lane + kKv4TmemO + c0, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            tmem_st32(t_lane + kKv4TmemO + c0, x);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        mo = fmaxf(mo, m);
+        uint4* w = reinterpret_cast<uint4*>((from_peer ? p_peer : p_own) + h * 16);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {                  // weights move up to the output's
+          const float mc = c < 4 ? ma : mb;
+          if (!(mc < mo)) continue;
+          const float f = fast_exp2(mc - mo);
+          uint4 y = w[c * kAttnHeads];
+          y.x = scale_bf16x2(y.x, f);
+          y.y = scale_bf16x2(y.y, f);
+          y.z = scale_bf16x2(y.z, f);
+          y.w = scale_bf16x2(y.w, f);
+          w[c * kAttnHeads] = y;
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&sm->fix_done);
+      }
+      if (!ok || !(ok = wait(&sm->fin_own, live) && wait_peer(&sm->fin_peer, live))) break;
+      // the output rows are relative to the largest reference; a NaN goes through
+      float m = -kInf, l = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, sm->fin[i >> 1][i & 1][1][h]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lp = sm->fin[i >> 1][i & 1][0][h], mp = sm->fin[i >> 1][i & 1][1][h];
+        l += lp > 0.f ? lp * fast_exp2(mp - m) : lp;
+      }
+      __syncwarp();
+      if (h == 0) mbar_arrive_expect_tx(&sm->fin_peer, kFinBytes);
+      if (lane == 0) {
+        mbar_arrive(&sm->fin_free);
+        mbar_arrive_remote(peer_fin_free);
+      }
       tc_fence_after();
-      l += lo;
       const float inv = 1.f / l;
 #pragma unroll 1
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(t_lane + kAttnTmemO + 128 * g + c0, v);
+      for (int c0 = 0; c0 < 256; c0 += 32) {
+        uint32_t x[32];
+        tmem_ld32(t_lane + kKv4TmemO + c0, x);
         tmem_wait_ld();
+        if (c0 == 224) {                               // all of it is in registers
+          tc_fence_before();
+          warp_arrive(&sm->o_empty);
+        }
         if (!head_ok) continue;
         if (p.parts > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.parts + part) * kAttnDv + col0 + c0);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.parts + it.part) * kAttnDv + rank * 256 + c0);
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4)
-            dst[q4] = make_float4(__uint_as_float(v[4 * q4]) * inv, __uint_as_float(v[4 * q4 + 1]) * inv,
-                                  __uint_as_float(v[4 * q4 + 2]) * inv, __uint_as_float(v[4 * q4 + 3]) * inv);
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(x[4 * i]) * inv, __uint_as_float(x[4 * i + 1]) * inv,
+                                 __uint_as_float(x[4 * i + 2]) * inv, __uint_as_float(x[4 * i + 3]) * inv);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + orow * kAttnDv + col0 + c0);
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(v[8 * q4 + 0]) * inv, __uint_as_float(v[8 * q4 + 1]) * inv);
-            w.y = pack_bf16x2(__uint_as_float(v[8 * q4 + 2]) * inv, __uint_as_float(v[8 * q4 + 3]) * inv);
-            w.z = pack_bf16x2(__uint_as_float(v[8 * q4 + 4]) * inv, __uint_as_float(v[8 * q4 + 5]) * inv);
-            w.w = pack_bf16x2(__uint_as_float(v[8 * q4 + 6]) * inv, __uint_as_float(v[8 * q4 + 7]) * inv);
-            dst[q4] = w;
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              w[q] = pack_bf16x2(__uint_as_float(x[16 * i + 2 * q]) * inv, __uint_as_float(x[16 * i + 2 * q + 1]) * inv);
+            stg256(out + c0 + 16 * i, w);
           }
         }
       }
-    } else if (T == 0 && head_ok && p.parts == 1) {
-      uint4* dst = reinterpret_cast<uint4*>(p.o + orow * kAttnDv + col0);
-      for (int q4 = 0; q4 < 16; ++q4) dst[q4] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    if (rank == 0 && g == 0 && head_ok && (have || T == 0)) {
-      const float v = T == 0 ? -kInf : (m + log2f(l)) * 0.69314718055994531f;
-      if (p.parts > 1) p.part_lse[orow * p.parts + part] = v;
-      else p.lse[orow] = v;
+      if (rank == 0 && head_ok) {
+        const float x = (m + log2f(l)) * 0.69314718055994531f;
+        if (p.parts > 1) p.part_lse[orow * p.parts + it.part] = x;
+        else p.lse[p.row0 * p.heads + orow] = x;
+      }
+      ++live;
     }
   }
   tc_fence_before();
@@ -552,28 +937,46 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
 }
 
 // Joins the parts of one (query, head): o = sum_i exp(lse_i - lse) o_i.  A part
-// without keys has lse_i = -inf and no output to read.
+// without keys has lse_i = -inf and no output to read.  Eight parts' loads are
+// in flight at a time.
+constexpr int kKv4MaxParts = kKv4MaxK / kAttnTileN;
 __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
-  const int64_t orow = blockIdx.x;
+  __shared__ float weight[kKv4MaxParts];
+  const int64_t orow = blockIdx.x, out = p.row0 * p.heads + orow;
+  const float kInf = __int_as_float(0x7f800000);
   const float* pl = p.part_lse + orow * p.parts;
-  float top = -__int_as_float(0x7f800000);
-  for (int i = 0; i < p.parts; ++i) top = fmaxf(top, pl[i]);
+  const float* po = p.part_o + orow * p.parts * kAttnDv + threadIdx.x * 4;
+  const int lane = threadIdx.x & 31;
+  float top = -kInf;
+  for (int i = lane; i < p.parts; i += 32) top = fmaxf(top, pl[i]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   float z = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (top > -__int_as_float(0x7f800000)) {
-    for (int i = 0; i < p.parts; ++i) {
-      const float w = expf(pl[i] - top);
-      if (w == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + (orow * p.parts + i) * kAttnDv + threadIdx.x * 4);
-      z += w;
-      acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
-    }
-    const float inv = 1.f / z;
-    acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
+  for (int i = lane; i < p.parts; i += 32) {
+    const float w = top > -kInf ? expf(pl[i] - top) : 0.f;
+    z += w;
+    if (threadIdx.x < 32) weight[i] = w;
   }
-  *reinterpret_cast<uint2*>(p.o + orow * kAttnDv + threadIdx.x * 4) =
-      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-  if (threadIdx.x == 0) p.lse[orow] = top + logf(z);   // -inf + log 0 = -inf for an empty set
+#pragma unroll
+  for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < p.parts; i0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = i0 + u < p.parts && weight[i0 + u] != 0.f ? *reinterpret_cast<const float4*>(po + static_cast<int64_t>(i0 + u) * kAttnDv)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float w = i0 + u < p.parts ? weight[i0 + u] : 0.f;
+      acc.x += w * v[u].x; acc.y += w * v[u].y; acc.z += w * v[u].z; acc.w += w * v[u].w;
+    }
+  }
+  const float inv = z > 0.f ? 1.f / z : z;               // no key at all: 0; a NaN goes through
+  *reinterpret_cast<uint2*>(p.o + out * kAttnDv + threadIdx.x * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (threadIdx.x == 0) p.lse[out] = top + logf(z);    // -inf + log 0 = -inf for an empty set
 }
 
 }  // namespace hisa

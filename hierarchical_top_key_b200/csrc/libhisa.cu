@@ -336,22 +336,29 @@ hisa_status check_kv4_attn(int32_t batch, int32_t num_queries, int32_t heads, in
   return HISA_OK;
 }
 
-// Parts of each row's keys: as many as give every pair of SMs one work item,
-// at least one 64-key tile each.
-int kv4_parts(int64_t rows, int32_t heads, int32_t top_k) {
-  const int64_t items = rows * ceil_div(heads, kAttnHeads);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / items, ceil_div(top_k, kAttnTileN))));
-}
+// Parts of each query's keys: as many as give every pair of SMs one work item,
+// at least one 64-key tile each; and the workspace of one query (its record
+// list and, with parts, their outputs).
+struct Kv4Plan {
+  int parts, list_ld;
+  size_t per_row;
+};
 
-size_t kv4_part_bytes(int64_t rows, int32_t heads, int parts) {
-  return parts == 1 ? 0 : static_cast<size_t>(rows) * heads * parts * (kAttnDv + 1) * 4;
+Kv4Plan kv4_plan(int64_t rows, int32_t heads, int32_t top_k) {
+  const int64_t items = rows * ceil_div(heads, kAttnHeads);
+  Kv4Plan p;
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / items, ceil_div(top_k, kAttnTileN))));
+  p.list_ld = static_cast<int>(pad4(top_k));
+  p.per_row = static_cast<size_t>(p.list_ld) * 4 + 4 +
+              (p.parts > 1 ? static_cast<size_t>(heads) * p.parts * (kAttnDv + 1) * 4 : 0);
+  return p;
 }
 
 hisa_status kv4_workspace(const hisa_shape* s, size_t* bytes) {
   if (!s) return fail(HISA_ERR_INVALID_ARG, "shape is NULL");
   hisa_status e = check_kv4_attn(s->batch, s->num_queries, s->heads, s->top_k);
   if (e != HISA_OK) return e;
-  *bytes = kv4_part_bytes(rows_of(s), s->heads, kv4_parts(rows_of(s), s->heads, s->top_k));
+  *bytes = static_cast<size_t>(rows_of(s)) * kv4_plan(rows_of(s), s->heads, s->top_k).per_row;
   return HISA_OK;
 }
 
@@ -1273,52 +1280,68 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
   if (!std::isfinite(scale)) return fail(HISA_ERR_INVALID_ARG, "scale must be finite");
   if (!q || !cache || !page_table || !idx || !o || !lse)
     return fail(HISA_ERR_INVALID_ARG, "q, cache, page_table, idx, o and lse must be non-NULL");
-  if (!aligned16(q) || !aligned32(cache) || !aligned16(o) || !aligned4(page_table) || !aligned4(idx) || !aligned4(lse))
+  if (!aligned16(q) || !aligned32(cache) || !aligned32(o) || !aligned4(page_table) || !aligned4(idx) || !aligned4(lse))
     return fail(HISA_ERR_INVALID_ARG,
-                "q and o must be 16-byte, cache 32-byte, page_table, idx and lse 4-byte aligned");
-  if (workspace && !aligned16(workspace)) return fail(HISA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+                "q must be 16-byte, cache and o 32-byte, page_table, idx and lse 4-byte aligned");
   const int64_t rows = static_cast<int64_t>(batch) * num_queries;
-  const int64_t slices = ceil_div(heads, kAttnHeads);
-  const int parts = workspace && ws_bytes >= kv4_part_bytes(rows, heads, kv4_parts(rows, heads, top_k))
-                        ? kv4_parts(rows, heads, top_k) : 1;
-  if (rows * slices * 2 > INT32_MAX || rows * heads > INT32_MAX)
-    return fail(HISA_ERR_UNSUPPORTED, "too many (query, head) pairs");
+  if (rows * heads > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many (query, head) pairs");
+  const Kv4Plan plan = kv4_plan(rows, heads, top_k);
+  const int64_t chunk = std::min<int64_t>(rows, static_cast<int64_t>(ws_bytes / plan.per_row));
+  if (!workspace || !aligned16(workspace) || chunk < 1)
+    return fail(HISA_ERR_WORKSPACE, "workspace holds less than one query (%zu bytes, 16-byte aligned)", plan.per_row);
   Kv4AttnParams p{};
-  p.rows = rows; p.Q = num_queries; p.L = num_keys; p.heads = heads; p.top_k = top_k;
+  p.Q = num_queries; p.L = num_keys; p.heads = heads; p.top_k = top_k; p.list_ld = plan.list_ld;
   p.page_size = page_size; p.num_pages = num_pages;
   p.pages_per_seq = static_cast<int>(ceil_div(num_keys, page_size));
-  p.slots = 64;
-  while (p.slots < 2 * top_k) p.slots *= 2;
-  p.slices = static_cast<int>(slices); p.parts = parts;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) p.page_shift = i;
+  p.slices = static_cast<int>(ceil_div(heads, kAttnHeads)); p.parts = plan.parts;
   // the kernel's masked logits are -inf, which a scale of 0 would turn into NaN
   p.scale_log2 = scale == 0.f ? 1.f : std::fabs(scale) * 1.4426950408889634f;
-  p.q_keep = scale == 0.f ? 0u : ~0u;
-  p.q_flip = scale < 0.f ? 0x80008000u : 0u;
+  p.sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
   p.idx = idx; p.page_table = page_table; p.cache = static_cast<const uint8_t*>(cache);
   p.q = static_cast<const uint16_t*>(q); p.o = static_cast<uint16_t*>(o); p.lse = lse;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o ? p.part_o + rows * heads * parts * kAttnDv : nullptr;
+  const size_t sel_smem = kv4_select_smem(top_k);
+  e = cuda_check(cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(sel_smem)), "kv4_select attribute");
+  if (e != HISA_OK) return e;
   e = cuda_check(cudaFuncSetAttribute(kv4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(kKv4SmemBytes)), "kv4_attn attribute");
   if (e != HISA_OK) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * slices * parts * 2));
-  cfg.blockDim = dim3(kKv4Threads);
-  cfg.dynamicSmemBytes = kKv4SmemBytes;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_attn_kernel, p), "launch kv4_attn_kernel");
-  if (e != HISA_OK) return e;
-  e = launch_check("kv4_attn_kernel");
-  if (e != HISA_OK || parts == 1) return e;
-  kv4_join_kernel<<<static_cast<unsigned>(rows * heads), 128, 0, cfg.stream>>>(p);
-  return launch_check("kv4_join_kernel");
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  for (p.row0 = 0; p.row0 < rows; p.row0 += chunk) {
+    const int64_t n = std::min<int64_t>(chunk, rows - p.row0);
+    // outputs of the parts, lists, then the odd-sized arrays
+    p.part_o = static_cast<float*>(workspace);
+    p.list = reinterpret_cast<int32_t*>(p.part_o + (plan.parts > 1 ? n * heads * plan.parts * kAttnDv : 0));
+    p.count = p.list + n * plan.list_ld;
+    p.part_lse = reinterpret_cast<float*>(p.count + n);
+    p.items = n * p.slices * p.parts;
+    kv4_select_kernel<<<static_cast<unsigned>(n), kKv4SelThreads, sel_smem, st>>>(p);
+    e = launch_check("kv4_select_kernel");
+    if (e != HISA_OK) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(p.items, num_sms() / 2)));
+    cfg.blockDim = dim3(kKv4Threads);
+    cfg.dynamicSmemBytes = kKv4SmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_attn_kernel, p), "launch kv4_attn_kernel");
+    if (e != HISA_OK) return e;
+    if (plan.parts > 1) {
+      kv4_join_kernel<<<static_cast<unsigned>(n * heads), 128, 0, st>>>(p);
+      e = launch_check("kv4_join_kernel");
+      if (e != HISA_OK) return e;
+    }
+  }
+  return HISA_OK;
 }
 
 }  // extern "C"

@@ -499,17 +499,17 @@ HISA_API hisa_status hisa_kv4_read(const void* cache, int64_t num_slots, const i
  *   cache       [num_pages, page_size, 416] bytes (hisa_kv4_write)
  *   page_table  [batch, ceil(L / page_size)] int32, L = num_keys
  *   idx         [batch, Q, top_k] int32, top_k <= 4096
- *   o           [batch, Q, heads, 512] bf16;  lse [batch, Q, heads] fp32
+ *   o           [batch, Q, heads, 512] bf16, 32-byte aligned;  lse [batch, Q, heads] fp32
  * Entries of idx outside [0, L) and repeats are dropped.  A page that is
  * needed and lies outside [0, num_pages) is not dereferenced: the position is
  * dropped and the device status word reports HISA_ERR_INVALID_ARG.
  * num_pages * page_size must fit in int32.
- * Workspace: optional, 16-byte aligned.
- * hisa_workspace_size(HISA_OP_SPARSE_ATTENTION_KV4), from the shape's batch,
- * num_queries, heads and top_k, is nonzero where there are few queries (a
- * decode step); given that much, each query's keys are split over several
- * pairs of SMs and the parts joined.  NULL (or less) runs each query whole.
- * The two agree to rounding.
+ * Workspace (16-byte aligned): hisa_workspace_size(HISA_OP_SPARSE_ATTENTION_KV4)
+ * bytes, from the shape's batch, num_queries, heads and top_k (the other fields
+ * are not read): each query's record list, and where there are few queries (a
+ * decode step), whose keys are then split over several pairs of SMs, the
+ * outputs of the parts.  With less the queries are processed in chunks that
+ * fit; less than one query's share is HISA_ERR_WORKSPACE.
  */
 HISA_API hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t num_pages,
                                                int32_t page_size, const int32_t* page_table,

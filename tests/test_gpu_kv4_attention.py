@@ -152,22 +152,28 @@ def test_split_and_whole_agree(lib):
         assert (d <= 2.0 ** -7 * o[0, t].float().abs() + 2.0 ** -6).all()
 
 
-def test_no_workspace(lib):
-    """Through the C entry without a workspace: each query whole."""
-    import ctypes
+@pytest.mark.parametrize("Q", [1, 7])
+def test_small_workspace(lib, Q):
+    """Queries in chunks of what the workspace holds: the same bits; nothing past it is touched."""
     hb = _hb()
     c = Case(2, 900, 64, 3)
-    q = _q(2, 1, 128, 3)
-    idx = synthetic.random_index_rows(2, 1, 900, 500, np.full((2, 1), 900), seed=3)
-    dq, di, dt = q.cuda(), torch.from_numpy(idx).cuda(), c.table.cuda()
-    o = torch.empty((2, 1, 128, 512), dtype=torch.bfloat16, device="cuda")
-    lse = torch.empty((2, 1, 128), device="cuda")
-    st = hb.load().hisa_sparse_attention_kv4(dq.data_ptr(), c.cache.data_ptr(), c.cache.shape[0], 64, dt.data_ptr(),
-                                             di.data_ptr(), 2, 1, 900, 128, 500, ctypes.c_float(SCALE), o.data_ptr(),
-                                             lse.data_ptr(), None, 0, torch.cuda.current_stream().cuda_stream)
-    assert st == 0
-    hb.get_status()
-    c.check(q, idx, o, lse, "no workspace")
+    q = _q(2, Q, 128, 3)
+    idx = synthetic.random_index_rows(2, Q, 900, 500, np.full((2, Q), 900), seed=3)
+    o, lse = c.run(q, idx)
+    c.check(q, idx, o, lse, "whole")
+    full = hb.workspace_size(hb.OP_ATTENTION_KV4, hb.Shape(2, 900, Q, 128, 0, 0, 0, 500, hb.HISA_BF16))
+    assert full % (2 * Q) == 0
+    for rows in (1, 2 * Q - 1):
+        n = full // (2 * Q) * rows
+        ws = torch.full((n + 64,), 0xC3, dtype=torch.uint8, device="cuda")
+        o2, l2 = hb.hisa_sparse_attention_kv4(q.cuda(), c.cache, c.table.cuda(), torch.from_numpy(idx).cuda(),
+                                              scale=SCALE, num_keys=900, workspace=ws[:n])
+        hb.get_status()
+        assert torch.equal(o, o2) and torch.equal(lse, l2) and (ws[n:] == 0xC3).all()
+    with pytest.raises(hb.HisaError) as e:
+        hb.hisa_sparse_attention_kv4(q.cuda(), c.cache, c.table.cuda(), torch.from_numpy(idx).cuda(), scale=SCALE,
+                                     num_keys=900, workspace=ws[:64])
+    assert e.value.status == 3
 
 
 def test_large_logits_and_jumps_of_the_maximum(lib):

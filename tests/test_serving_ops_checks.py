@@ -85,6 +85,7 @@ def test_attention_arguments(L):
     assert call(q=0x1008) == 1 and call(cache=0x2008) == 1 and call(idx=0x4002) == 1 and call(table=0x3002) == 1
     assert call(o=0x5008) == 1 and call(lse=0x6002) == 1 and call(ws=0x7008, wsb=1 << 20) == 3
     assert call(batch=1 << 20, Q=1 << 20) == 2
+    assert call() == 3 and call(ws=0x7000, wsb=64 * 4 + 3) == 3
 
 
 def test_attention_workspace_rule(L):
@@ -93,8 +94,11 @@ def test_attention_workspace_rule(L):
                  dtype=hb.HISA_BF16)
         s.update(kw)
         return hb.workspace_size(hb.OP_ATTENTION_KV4, hb.Shape(**s))
-    assert size(num_queries=4096) == 0                      # every pair of SMs has a query of its own
-    assert size(top_k=64) == 0                              # one tile of keys: nothing to split
+    # a record list and its length for each query; parts' outputs only where there are few queries and keys to split
+    assert size(num_queries=4096) == 4096 * (2048 * 4 + 4)
+    assert size(top_k=64) == 64 * 4 + 4 and size(top_k=1) == 4 * 4 + 4
+    one = size() - (2048 * 4 + 4)
+    assert one > 0 and one % (128 * 513 * 4) == 0 and 2 <= one // (128 * 513 * 4) <= 32
     n = ctypes.c_size_t(0)
     for bad, status in ((dict(heads=0), 1), (dict(batch=0), 1), (dict(top_k=4097), 2)):
         s = dict(batch=1, num_keys=1000, num_queries=1, heads=128, head_dim=0, block_size=0, top_m=0, top_k=2048, dtype=1)
