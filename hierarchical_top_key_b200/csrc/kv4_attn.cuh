@@ -216,7 +216,7 @@ constexpr uint32_t kKv4P = kAttnHeads * kAttnTileN * 2;   // a tile's weights
 
 struct Kv4Smem {
   uint64_t q_full, q_free, o_empty;            // a query is in place; its last own logits are done; its output has been read
-  uint64_t kx_full, vo_full[2], vo_empty[2];   // own tiles (the rest of a row: kx; s_full frees it)
+  uint64_t kx_full, kx_empty, vo_full[2], vo_empty[2];   // own tiles (kx: the rest of a row)
   uint64_t vr_full, vr_empty;                  // the peer's tiles
   uint64_t s_full, s_empty;
   uint64_t p_own, p_peer, p_free;              // weights of an own tile, of a peer's tile; both CTAs have used mine
@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     mbar_init(&sm->q_free, 1);
     mbar_init(&sm->o_empty, 4);
     mbar_init(&sm->kx_full, 4);
+    mbar_init(&sm->kx_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->vo_full[i], 4);
       mbar_init(&sm->vo_empty[i], 1);
@@ -481,18 +482,22 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
         tc_fence_after();
         for (int k = 0; k < own; ++k, ++u) {
           const uint64_t vo_desc = desc_k_sw128(smem_u32(vo_buf + (u & 1) * kKv4V));
-          if (!(ok = mbar_wait(&sm->vo_full[u & 1], (u >> 1) & 1, abort_flag))) break;
+          if (!(ok = mbar_wait(&sm->kx_full, u & 1, abort_flag))) break;
           if (u >= 1 && !(ok = mbar_wait(&sm->s_empty, (u - 1) & 1, abort_flag))) break;
           tc_fence_after();
-          // the value half's four panels, which are there early; meanwhile
-          // the rest of the row is made: the other half's four and the
-          // positional one, whose single buffer the logits before have freed
+          // the positional panel and the other half's four first: their single
+          // buffer is then free for the next tile while the value half's run
 #pragma unroll
           for (int pn = 0; pn < 9; ++pn) {
-            if (pn == 4 && !(ok = mbar_wait(&sm->kx_full, u & 1, abort_flag))) break;
-            const uint32_t panel = pn < 4 ? 4 * rank + pn : pn < 8 ? 4 * peer + pn - 4 : 8u;    // of the row
-            const uint64_t kd = pn < 4 ? vo_desc + static_cast<uint64_t>(pn * (kKv4Panel / 16))
-                                       : kx_desc + static_cast<uint64_t>((pn - 4) * (kKv4Panel / 16));
+            if (pn == 5) {
+              mma_commit(&sm->kx_empty);
+              if (!(ok = mbar_wait(&sm->vo_full[u & 1], (u >> 1) & 1, abort_flag))) break;
+              tc_fence_after();
+            }
+            const uint32_t panel = pn == 0 ? 8u : pn < 5 ? 4 * peer + pn - 1 : 4 * rank + pn - 5;    // of the row
+            const uint64_t kd = pn == 0  ? kx_desc + static_cast<uint64_t>(4 * (kKv4Panel / 16))
+                                : pn < 5 ? kx_desc + static_cast<uint64_t>((pn - 1) * (kKv4Panel / 16))
+                                         : vo_desc + static_cast<uint64_t>((pn - 5) * (kKv4Panel / 16));
             if (panel < kKv4QPanels) {
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
             at += (n & 1) * kKv4V;
             full = &sm->vo_full[n & 1];
           } else {
-            if (n >= 1 && !(ok = wait(&sm->s_full, n - 1))) break;     // the logits of the own tile before are done
+            if (n >= 1 && !(ok = wait(&sm->kx_empty, n - 1))) break;
             full = &sm->kx_full;
             sts128(rope_at, ra[0], ra[1], ra[2], ra[3]);
             sts128(rope_at ^ 16u, ra[4], ra[5], ra[6], ra[7]);
