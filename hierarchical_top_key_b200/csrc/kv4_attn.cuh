@@ -276,6 +276,26 @@ __device__ __forceinline__ void stg256(void* dst, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// Pairs of fp32 in a 64-bit register: one instruction for two (sm_100).
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Two bf16 times f, each rounded once.
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t x, float f) {
   return pack_bf16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
@@ -767,16 +787,21 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
           l *= fast_exp2(m - mt);
           m = mt;
         }
-        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          s[i] = fast_exp2(__fmaf_rn(s[i], p.scale_log2, -m));
-          sum4[i & 3] += s[i];
-        }
-        l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
         uint32_t w[16];
+        uint64_t sum2[2] = {0, 0};                     // pairs of fp32
+        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), m2 = pack_f32x2(-m, -m);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
+        for (int i = 0; i < 16; ++i) {
+          float a, b;
+          unpack_f32x2(fma_f32x2(pack_f32x2(s[2 * i], s[2 * i + 1]), scale2, m2), a, b);
+          a = fast_exp2(a);
+          b = fast_exp2(b);
+          sum2[i & 1] = add_f32x2(sum2[i & 1], pack_f32x2(a, b));
+          w[i] = pack_bf16x2(a, b);
+        }
+        float sa, sb;
+        unpack_f32x2(add_f32x2(sum2[0], sum2[1]), sa, sb);
+        l += sa + sb;
         // both CTAs' output MMAs have read the weights before
         if (u >= 1 && !(ok = wait_peer(&sm->p_free, u - 1))) break;
         const uint32_t mark = __any_sync(kFull, m != m_first) ? u + 1 : 0;
