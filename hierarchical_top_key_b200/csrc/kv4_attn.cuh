@@ -33,8 +33,8 @@
 // serves the whole query unless a later logit exceeds it by more than 2^64
 // (sums then stay below 2^64 * 2^12 keys * 2^15, the largest value).  Only the
 // warp that meets it moves its m; weights come with the m they were made with,
-// and a mark where that has moved; before the MMA of marked weights the output
-// or the weights are scaled to one reference.
+// and a mark where that has moved; from a query's first marked weights on, the
+// output or the weights are scaled to one reference before each MMA.
 //
 // Warp roles (26 warps a CTA, a persistent pair over queries):
 //   warp 0       TMEM owner, logit MMA issuer (one thread)
@@ -77,6 +77,12 @@ struct Kv4AttnParams {
   float* part_lse;           // [queries of this launch, heads, parts]
 };
 
+// The three kernels are launched with programmatic serialisation: a kernel
+// starts while the one before it ends, does what does not depend on it, and
+// waits here for its end.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- selection
 
 constexpr int kKv4SelThreads = 512, kKv4SelWarps = kKv4SelThreads / 32;
@@ -98,6 +104,7 @@ __global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4Att
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(16) int count[kKv4Per * kKv4SelWarps], place[kKv4Per * kKv4SelWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_next_kernel_start();
   const int K = p.top_k;
   const int64_t row = p.row0 + blockIdx.x;
   uint32_t* table = reinterpret_cast<uint32_t*>(smem_raw);
@@ -469,9 +476,17 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(&sm->tmem_base, 512);
+  if (tid >= kKv4CorrBase) {                           // the first query towards L2
+    const int slice = static_cast<int>(item0 / p.parts % p.slices), h = slice * kAttnHeads + tid - kKv4CorrBase;
+    const uint16_t* qh = p.q + ((p.row0 + item0 / p.parts / p.slices) * p.heads + h) * kAttnDqk;
+    if (h < p.heads)
+      for (int i = 0; i < 9; ++i) prefetch_l2(qh + 64 * i);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                      // the peer's barriers exist before any remote arrive
+  let_next_kernel_start();
+  wait_for_previous_kernel();                          // the lists
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
   auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {    // by all lanes, the outcome warp-uniform
@@ -554,6 +569,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
         // the previous query's output has been read
         if (live > 0 && !(ok = mbar_wait(&sm->o_empty, (live - 1) & 1, abort_flag))) break;
         ++live;
+        bool scaled = false;                           // from a query's first marked tile on all are looked at
         for (int t = 0; t < tiles; ++t) {
           const bool mine = (t & 1u) == rank;
           if (!(ok = mine ? mbar_wait(&sm->p_own, u & 1, abort_flag)
@@ -561,8 +577,9 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
             break;
           const uint4 m0 = lds128(smem_u32(sm->moved[mine ? 0 : 1])), m1 = lds128(smem_u32(sm->moved[mine ? 0 : 1] + 4));
           const uint32_t tag = (mine ? u : v) + 1;
-          if (m0.x == tag || m0.y == tag || m0.z == tag || m0.w == tag || m1.x == tag || m1.y == tag || m1.z == tag ||
+          if (scaled || m0.x == tag || m0.y == tag || m0.z == tag || m0.w == tag || m1.x == tag || m1.y == tag || m1.z == tag ||
               m1.w == tag) {
+            scaled = true;
             mma_commit(&sm->drain[1]);                 // every MMA before
             if (!(ok = mbar_wait(&sm->drain[1], drains++ & 1, abort_flag))) break;
             sm->command = kKv4Scale + (t == 0 ? kKv4First : 0) + (mine ? 0 : kKv4Peer);
@@ -977,6 +994,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
   const float* pl = p.part_lse + orow * p.parts;
   const float* po = p.part_o + orow * p.parts * kAttnDv + threadIdx.x * 4;
   const int lane = threadIdx.x & 31;
+  wait_for_previous_kernel();
   float top = -kInf;
   for (int i = lane; i < p.parts; i += 32) top = fmaxf(top, pl[i]);
 #pragma unroll

@@ -337,7 +337,7 @@ hisa_status check_kv4_attn(int32_t batch, int32_t num_queries, int32_t heads, in
 }
 
 // Parts of each query's keys: as many as give every pair of SMs one work item,
-// at least one 64-key tile each; and the workspace of one query (its record
+// at least two 64-key tiles each (one for either SM); and the workspace of one query (its record
 // list and, with parts, their outputs).
 struct Kv4Plan {
   int parts, list_ld;
@@ -347,7 +347,7 @@ struct Kv4Plan {
 Kv4Plan kv4_plan(int64_t rows, int32_t heads, int32_t top_k) {
   const int64_t items = rows * ceil_div(heads, kAttnHeads);
   Kv4Plan p;
-  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / items, ceil_div(top_k, kAttnTileN))));
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2 / items, ceil_div(top_k, 2 * kAttnTileN))));
   p.list_ld = static_cast<int>(pad4(top_k));
   p.per_row = static_cast<size_t>(p.list_ld) * 4 + 4 +
               (p.parts > 1 ? static_cast<size_t>(heads) * p.parts * (kAttnDv + 1) * 4 : 0);
@@ -1321,23 +1321,28 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
     kv4_select_kernel<<<static_cast<unsigned>(n), kKv4SelThreads, sel_smem, st>>>(p);
     e = launch_check("kv4_select_kernel");
     if (e != HISA_OK) return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(p.items, num_sms() / 2)));
     cfg.blockDim = dim3(kKv4Threads);
     cfg.dynamicSmemBytes = kKv4SmemBytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_attn_kernel, p), "launch kv4_attn_kernel");
     if (e != HISA_OK) return e;
     if (plan.parts > 1) {
-      kv4_join_kernel<<<static_cast<unsigned>(n * heads), 128, 0, st>>>(p);
-      e = launch_check("kv4_join_kernel");
+      cfg.gridDim = dim3(static_cast<unsigned>(n * heads));
+      cfg.blockDim = dim3(128);
+      cfg.dynamicSmemBytes = 0;
+      cfg.numAttrs = 1;
+      e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_join_kernel, p), "launch kv4_join_kernel");
       if (e != HISA_OK) return e;
     }
   }

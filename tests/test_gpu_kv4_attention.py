@@ -176,10 +176,12 @@ def test_small_workspace(lib, Q):
     assert e.value.status == 3
 
 
-def test_large_logits_and_jumps_of_the_maximum(lib):
+@pytest.mark.parametrize("Q", [2, 90])
+def test_large_logits_and_jumps_of_the_maximum(lib, Q):
     """Keys aligned with the mean head direction at chosen places, each raising
     the maximum by some tens; heads the other way keep theirs.  Then a tile
-    whose logits are hundreds below the others."""
+    whose logits are hundreds below the others.  Two queries are split over the
+    keys, 90 are not."""
     L, K = 3000, 1500
     c = Case(1, L, 64, 21)
     q = _q(1, 2, 128, 21)
@@ -191,8 +193,10 @@ def test_large_logits_and_jumps_of_the_maximum(lib):
         c.rewrite(0, int(idx[0, 0, place]), size * u)
     for place in range(12 * 64, 13 * 64):
         c.rewrite(0, int(idx[0, 0, place]), -300.0 * u)
+    q, idx = q.repeat(1, Q // 2, 1, 1), np.tile(idx, (1, Q // 2, 1))
     o, lse = c.run(q, idx)
-    c.check(q, idx, o, lse, "planted maxima")
+    c.check(q, idx, o, lse, "planted maxima", rows=[(0, t) for t in (0, 1, Q - 2, Q - 1)])
+    assert all(torch.equal(o[0, t], o[0, t % 2]) for t in range(Q))
     assert np.median(lse.cpu().numpy()[0, 0]) > 20.0
 
 
