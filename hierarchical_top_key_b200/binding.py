@@ -115,13 +115,32 @@ def _check(status: int, where: str):
         raise HisaError(status, where, msg)
 
 
+# the current stream's handle without building a Stream object for it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+class _Here:
+    """A context that changes nothing."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
 
 
 def _device_of(t: torch.Tensor):
     """Makes t's device current (its current stream is then the one used)."""
-    return torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -470,10 +489,10 @@ def _rows_of(x: torch.Tensor, name: str):
     return tokens, heads, dim, ts, x.stride(-2)
 
 
-def _on(device, name: str, *tensors):
+def _on(device: int, name: str, *tensors):
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors of {name} must be on one device, got {device} and {t.device}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors of {name} must be on one device (cuda:{device}), got one on {t.device}")
 
 
 def _rotary(name, x, positions, inv_freq, offset, out, weight=None, bias=None):
@@ -485,11 +504,13 @@ def _rotary(name, x, positions, inv_freq, offset, out, weight=None, bias=None):
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2]")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and dtype")
-    _, _, _, ots, ohs = _rows_of(out, "out")
-    _on(x.device, name, positions, inv_freq, out, weight, bias)
+        out = x.new_empty(x.shape)
+        ots, ohs = heads * dim, dim
+    else:
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have x's shape and dtype")
+        _, _, _, ots, ohs = _rows_of(out, "out")
+    _on(x.get_device(), name, positions, inv_freq, out, weight, bias)
     return tokens, heads, dim, ts, hs, out, ots, ohs
 
 
@@ -544,7 +565,7 @@ def _check_kv4_rows(rows: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor
         raise ValueError(f"rows must be a bfloat16 CUDA tensor [n, {KV4_WIDTH}] with contiguous features")
     if slots.dtype != torch.int32 or tuple(slots.shape) != (rows.shape[0],) or not slots.is_contiguous():
         raise ValueError("slots must be contiguous int32 [n]")
-    _on(cache.device, "the 4-bit cache", rows, slots)
+    _on(cache.get_device(), "the 4-bit cache", rows, slots)
     return rows.stride(0) if rows.shape[0] > 1 else KV4_WIDTH
 
 
@@ -564,7 +585,7 @@ def hisa_kv4_read(cache, slots, out: Optional[torch.Tensor] = None):
     (zeros for slots below 0)."""
     _check_kv4(cache)
     if out is None:
-        out = torch.empty((slots.shape[0], KV4_WIDTH), dtype=torch.bfloat16, device=cache.device)
+        out = cache.new_empty((slots.shape[0], KV4_WIDTH), dtype=torch.bfloat16)
     stride = _check_kv4_rows(out, slots, cache)
     with _device_of(cache):
         _check(load().hisa_kv4_read(cache.data_ptr(), cache.shape[0] * cache.shape[1], slots.data_ptr(), out.shape[0],
@@ -591,7 +612,7 @@ def hisa_sparse_attention_kv4(q, cache, page_table, idx, *, scale: float, num_ke
     pages = -(-num_keys // cache.shape[1])
     if page_table.dtype != torch.int32 or tuple(page_table.shape) != (b, pages):
         raise ValueError(f"page_table must be int32 {(b, pages)}, got {page_table.dtype} {tuple(page_table.shape)}")
-    _on(q.device, "hisa_sparse_attention_kv4", cache, page_table, idx, workspace)
+    _on(q.get_device(), "hisa_sparse_attention_kv4", cache, page_table, idx, workspace)
     with _device_of(q):
         o = torch.empty((b, Q, H, KV4_LATENT), dtype=torch.bfloat16, device=q.device)
         lse = torch.empty((b, Q, H), dtype=torch.float32, device=q.device)

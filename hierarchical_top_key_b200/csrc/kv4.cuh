@@ -79,77 +79,117 @@ struct Kv4RowParams {
 };
 
 constexpr int kKv4Warps = 8;
+constexpr int kKv4Rows = 2;                    // rows of a warp, all their loads in flight together
 
-// One warp per row, one 16-feature group per lane: the group's maximum, scale
-// and codes need no other lane.  Slots below 0 are skipped (padding), slots
-// past the cache are skipped and reported.
-__global__ void __launch_bounds__(32 * kKv4Warps) kv4_write_kernel(const Kv4RowParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kKv4Warps + (threadIdx.x >> 5);
-  if (row >= p.n) return;
-  const int64_t slot = __ldg(p.slots + row);
-  if (slot < 0) return;
-  if (slot >= p.num_slots) {
-    if (lane == 0) record_status(HISA_ERR_INVALID_ARG);
-    return;
-  }
-  const uint8_t* src = p.rows + row * p.row_stride;
-  uint8_t* dst = p.cache + slot * kKv4Record;
-  const uint4 a = *reinterpret_cast<const uint4*>(src + lane * 32), b = *reinterpret_cast<const uint4*>(src + lane * 32 + 16);
-  float v[16];
-  Vec16<DT_BF16>::unpack(a, v);
-  Vec16<DT_BF16>::unpack(b, v + 8);
-  float amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(v[j]));     // fmaxf drops a NaN
-  const uint32_t code = kv4_scale_code(amax);
-  const float s = __int_as_float(static_cast<int>(code << 20) + ((127 - 20) << 23));
+// The 16 codes of a group with scale code `code`, two words.  n = x / s to the
+// nearest even without a division: x / s, x of 8 significant bits and s of 4,
+// is a half step or at least 2^-10 from one; x * (1 / s) in an fma that
+// rounds to multiples of 2^-13 (the addend's unit) is therefore on the same
+// side of it, and exactly there if x / s is.  Adding 1.5 * 2^23 rounds to
+// even integers' bits.  Needs |x| <= 7 s.
+__device__ __forceinline__ uint2 kv4_codes(const float (&v)[16], float s) {
+  const float inv = 1.f / s;
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    // x has 8 significant bits and s four: the fp32 quotient is never rounded
-    // onto a half step that x / s is not on
-    float n = rintf(v[j] / s);
-    n = n == n ? fminf(fmaxf(n, -7.f), 7.f) : 0.f;
-    const int at = 4 * ((j & 7) >> 1) + 16 * (j & 1);
-    w[j >> 3] |= (static_cast<uint32_t>(static_cast<int>(n)) & 15u) << at;
+    const float y = __fadd_rn(__fmaf_rn(v[j], inv, 1536.f), -1536.f);
+    const uint32_t n = __float_as_uint(__fadd_rn(y, 12582912.f)) & 15u;
+    w[j >> 3] |= n << (4 * ((j & 7) >> 1) + 16 * (j & 1));
   }
-  *reinterpret_cast<uint2*>(dst + lane * 8) = make_uint2(w[0], w[1]);
-  dst[kKv4ScaleAt + lane] = static_cast<uint8_t>(code);
-  if (lane < 8)
-    *reinterpret_cast<uint4*>(dst + kKv4RopeAt + lane * 16) =
-        *reinterpret_cast<const uint4*>(src + 2 * kKv4Latent + lane * 16);
+  return make_uint2(w[0], w[1]);
 }
 
-// One warp per row, one 16-feature group per lane.  A slot below 0 gives a
-// zero row, one past the cache too and is reported.
+// The same with saturation, and a NaN as 0.
+__device__ __forceinline__ uint2 kv4_codes_any(const float (&v)[16], float s) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float n = rintf(v[j] / s);
+    n = n == n ? fminf(fmaxf(n, -7.f), 7.f) : 0.f;
+    w[j >> 3] |= (static_cast<uint32_t>(static_cast<int>(n)) & 15u) << (4 * ((j & 7) >> 1) + 16 * (j & 1));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A warp has kKv4Rows rows, a lane one 16-feature group of each: the group's
+// maximum, scale and codes need no other lane.  Bound by the 1152 + 416 bytes a
+// row; MEASURED_WRITE.  Slots below 0 are skipped (padding), slots past the
+// cache are skipped and reported.
+__global__ void __launch_bounds__(32 * kKv4Warps) kv4_write_kernel(const Kv4RowParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  uint4 a[kKv4Rows], b[kKv4Rows], rope[kKv4Rows];
+  int64_t slot[kKv4Rows];
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u) {
+    slot[u] = row0 + u < p.n ? __ldg(p.slots + row0 + u) : -1;
+    if (row0 + u >= p.n) continue;                     // a padding row is read too: the load does not wait for its slot
+    const uint8_t* src = p.rows + (row0 + u) * p.row_stride;
+    a[u] = __ldg(reinterpret_cast<const uint4*>(src + lane * 32));
+    b[u] = __ldg(reinterpret_cast<const uint4*>(src + lane * 32 + 16));
+    if (lane < 8) rope[u] = __ldg(reinterpret_cast<const uint4*>(src + 2 * kKv4Latent + lane * 16));
+  }
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u) {
+    if (slot[u] < 0) continue;
+    if (slot[u] >= p.num_slots) {
+      if (lane == 0) record_status(HISA_ERR_INVALID_ARG);
+      continue;
+    }
+    uint8_t* dst = p.cache + slot[u] * kKv4Record;
+    float v[16];
+    Vec16<DT_BF16>::unpack(a[u], v);
+    Vec16<DT_BF16>::unpack(b[u], v + 8);
+    float amax = 0.f;
+    bool odd = false;                                  // a NaN
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      amax = fmaxf(amax, fabsf(v[j]));                 // fmaxf drops a NaN
+      odd |= !(v[j] == v[j]);
+    }
+    const uint32_t code = kv4_scale_code(amax);
+    const float s = __int_as_float(static_cast<int>(code << 20) + ((127 - 20) << 23));
+    const uint2 w = odd || amax > 7.f * s ? kv4_codes_any(v, s) : kv4_codes(v, s);
+    *reinterpret_cast<uint2*>(dst + lane * 8) = w;
+    dst[kKv4ScaleAt + lane] = static_cast<uint8_t>(code);
+    if (lane < 8) *reinterpret_cast<uint4*>(dst + kKv4RopeAt + lane * 16) = rope[u];
+  }
+}
+
+// A warp has kKv4Rows rows, a lane 32 bytes (16 features) of each.  A slot below
+// 0 gives a zero row, one past the cache too and is reported.  MEASURED_READ.
 __global__ void __launch_bounds__(32 * kKv4Warps) kv4_read_kernel(const Kv4RowParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kKv4Warps + (threadIdx.x >> 5);
-  if (row >= p.n) return;
-  const int64_t slot = __ldg(p.slots + row);
-  uint8_t* dst = p.rows + row * p.row_stride;
-  uint32_t o[8] = {};
-  uint4 rope = make_uint4(0u, 0u, 0u, 0u);
-  if (slot >= 0 && slot < p.num_slots) {
-    const uint8_t* src = p.cache + slot * kKv4Record;
-    const uint2 w = *reinterpret_cast<const uint2*>(src + lane * 8);
-    uint32_t s16, m24;
-    kv4_scales(src[kKv4ScaleAt + lane], 0, s16, m24);
-    uint32_t d[4];
-    kv4_decode8(w.x, s16, m24, d);
+  const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
+  int64_t slot[kKv4Rows];
+  uint2 w[kKv4Rows];
+  uint32_t code[kKv4Rows];
+  uint4 rope[kKv4Rows];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = d[j];
-    kv4_decode8(w.y, s16, m24, d);
+  for (int u = 0; u < kKv4Rows; ++u) slot[u] = row0 + u < p.n ? __ldg(p.slots + row0 + u) : -1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[4 + j] = d[j];
-    if (lane < 8) rope = *reinterpret_cast<const uint4*>(src + kKv4RopeAt + lane * 16);
-  } else if (slot >= p.num_slots && lane == 0) {
-    record_status(HISA_ERR_INVALID_ARG);
+  for (int u = 0; u < kKv4Rows; ++u) {
+    const bool in = slot[u] >= 0 && slot[u] < p.num_slots;
+    const uint8_t* src = p.cache + (in ? slot[u] : 0) * kKv4Record;      // record 0 for a zero row: not used
+    w[u] = __ldg(reinterpret_cast<const uint2*>(src + lane * 8));
+    code[u] = __ldg(src + kKv4ScaleAt + lane);
+    if (lane < 8) rope[u] = __ldg(reinterpret_cast<const uint4*>(src + kKv4RopeAt + lane * 16));
   }
-  *reinterpret_cast<uint4*>(dst + lane * 32) = make_uint4(o[0], o[1], o[2], o[3]);
-  *reinterpret_cast<uint4*>(dst + lane * 32 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-  if (lane < 8) *reinterpret_cast<uint4*>(dst + 2 * kKv4Latent + lane * 16) = rope;
+#pragma unroll
+  for (int u = 0; u < kKv4Rows; ++u) {
+    if (row0 + u >= p.n) break;
+    const bool in = slot[u] >= 0 && slot[u] < p.num_slots;
+    if (slot[u] >= p.num_slots && lane == 0) record_status(HISA_ERR_INVALID_ARG);
+    uint8_t* dst = p.rows + (row0 + u) * p.row_stride;
+    uint32_t s16, m24, d[4], e[4];
+    kv4_scales(code[u], 0, s16, m24);
+    kv4_decode8(w[u].x, s16, m24, d);
+    kv4_decode8(w[u].y, s16, m24, e);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(dst + lane * 32) = in ? make_uint4(d[0], d[1], d[2], d[3]) : zero;
+    *reinterpret_cast<uint4*>(dst + lane * 32 + 16) = in ? make_uint4(e[0], e[1], e[2], e[3]) : zero;
+    if (lane < 8) *reinterpret_cast<uint4*>(dst + 2 * kKv4Latent + lane * 16) = in ? rope[u] : zero;
+  }
 }
 
 }  // namespace hisa

@@ -1157,8 +1157,77 @@ hisa_status check_rows(const void* x, int64_t xt, int64_t xh, const void* out, i
 
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(n - 1)) == 0; }
 
+template <int DT, int V, int PAIRS>
+hisa_status launch_rotary_vec(const RotaryParams& p, int norm, int log_g, int nvec, cudaStream_t st) {
+  // some rows a lane group, as few as still fill the SMs; at most as many
+  // tokens as the block's table of turns holds
+  const int groups = kRotaryThreads >> log_g, half = p.rot / 2;
+  const int64_t per = std::min<int64_t>(8, std::max<int64_t>(1, p.rows / (static_cast<int64_t>(groups) * num_sms() * 8)));
+  const int64_t max_tokens = kRotaryTable / half;
+  const int64_t rows = std::min(groups * per, p.heads == 1 ? max_tokens : (max_tokens - 1) * p.heads);
+  const int64_t blocks = ceil_div(p.rows, rows);
+  if (blocks > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
+  const int64_t tokens = p.heads == 1 ? rows : std::min<int64_t>((rows + p.heads - 2) / p.heads + 1, max_tokens);
+  const size_t smem = static_cast<size_t>(half) * 8 * (1 + tokens);
+  const unsigned g = static_cast<unsigned>(blocks);
+  const int r = static_cast<int>(rows);
+  switch (norm) {
+    case NORM_NONE:
+      norm_rotary_vec_kernel<DT, NORM_NONE, V, PAIRS><<<g, kRotaryThreads, smem, st>>>(p, log_g, nvec, r);
+      break;
+    case NORM_RMS:
+      norm_rotary_vec_kernel<DT, NORM_RMS, V, PAIRS><<<g, kRotaryThreads, smem, st>>>(p, log_g, nvec, r);
+      break;
+    default: norm_rotary_vec_kernel<DT, NORM_LAYER, V, PAIRS><<<g, kRotaryThreads, smem, st>>>(p, log_g, nvec, r); break;
+  }
+  return launch_check("norm_rotary_vec_kernel");
+}
+
+template <int DT, int PAIRS>
+hisa_status launch_rotary_lanes(const RotaryParams& p, int norm, int v, int log_g, int nvec, cudaStream_t st) {
+  switch (v) {                                         // 8 vectors of 32 lanes cover the widest row
+    case 1: return launch_rotary_vec<DT, 1, PAIRS>(p, norm, log_g, nvec, st);
+    case 2: return launch_rotary_vec<DT, 2, PAIRS>(p, norm, log_g, nvec, st);
+    case 3: return launch_rotary_vec<DT, 3, PAIRS>(p, norm, log_g, nvec, st);
+    case 4: return launch_rotary_vec<DT, 4, PAIRS>(p, norm, log_g, nvec, st);
+    default: return launch_rotary_vec<DT, 8, PAIRS>(p, norm, log_g, nvec, st);
+  }
+}
+
 template <int DT>
 hisa_status launch_rotary_dt(const RotaryParams& p, int norm, cudaStream_t st) {
+  const int64_t es = Elem<DT>::bytes;
+  auto whole = [&](int64_t n) { return n * es % 16 == 0; };
+  const bool vec = aligned16(p.x) && aligned16(p.out) && (p.rows == p.heads || (whole(p.x_token) && whole(p.out_token))) &&
+                   (p.heads == 1 || (whole(p.x_head) && whole(p.out_head))) && whole(p.first) && whole(p.last) &&
+                   whole(p.offset) && whole(p.rot) && (p.interleaved || whole(p.rot / 2)) && kRotaryTable / (p.rot / 2) >= 2 &&
+                   (norm == NORM_NONE || (whole(p.norm_dim) && aligned16(p.weight) && aligned16(p.bias)));
+  if (vec) {
+    const int nvec = static_cast<int>((p.last - p.first) * es / 16);
+    // half-layout partners in one lane: as many lanes as vectors between them,
+    // the part at an even number of those
+    const int hv = static_cast<int>(p.rot / 2 * es / 16), ro = static_cast<int>((p.offset - p.first) * es / 16);
+    if (!p.interleaved && hv <= 32 && (hv & (hv - 1)) == 0 && ro % (2 * hv) == 0 && nvec % hv == 0 && nvec <= 4 * hv) {
+      int lg = 0;
+      while ((1 << lg) < hv) ++lg;
+      return nvec <= 2 * hv ? launch_rotary_vec<DT, 2, PAIRS_IN_LANE>(p, norm, lg, nvec, st)
+                            : launch_rotary_vec<DT, 4, PAIRS_IN_LANE>(p, norm, lg, nvec, st);
+    }
+    // vectors a lane: the count that wastes the fewest lanes; of equals one
+    // that leaves 8 lanes (128 bytes) a row
+    const int choices[] = {2, 1, 4, 3, 8};
+    int best = 0, best_lg = 0, best_slots = INT32_MAX;
+    for (int v : choices) {
+      int lg = 0;
+      while ((v << lg) < nvec && lg < 5) ++lg;
+      if ((v << lg) < nvec) continue;
+      if ((v << lg) < best_slots || ((v << lg) == best_slots && best_lg > 3 && lg >= 3)) {
+        best = v; best_lg = lg; best_slots = v << lg;
+      }
+    }
+    return p.interleaved ? launch_rotary_lanes<DT, PAIRS_INTERLEAVED>(p, norm, best, best_lg, nvec, st)
+                         : launch_rotary_lanes<DT, PAIRS_RELOAD>(p, norm, best, best_lg, nvec, st);
+  }
   const int64_t blocks = ceil_div(p.rows, kRotaryWarps);
   if (blocks > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
   const unsigned g = static_cast<unsigned>(blocks);
@@ -1217,7 +1286,7 @@ hisa_status check_kv4_rows(const void* rows, int64_t row_stride, const int32_t* 
   if (!rows || !slots || !cache) return fail(HISA_ERR_INVALID_ARG, "rows, slots and cache must be non-NULL");
   if (!aligned16(rows) || !aligned32(cache) || !aligned4(slots))
     return fail(HISA_ERR_INVALID_ARG, "rows must be 16-byte, cache 32-byte and slots 4-byte aligned");
-  if (ceil_div(n, kKv4Warps) > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
+  if (ceil_div(n, kKv4Warps * kKv4Rows) > INT32_MAX) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
   return HISA_OK;
 }
 
@@ -1251,7 +1320,7 @@ hisa_status hisa_kv4_write(const void* rows, int64_t row_stride, const int32_t* 
   if (e != HISA_OK || n == 0) return e;
   Kv4RowParams p{slots, static_cast<uint8_t*>(cache), static_cast<uint8_t*>(const_cast<void*>(rows)), n, num_slots,
                  row_stride * 2};
-  kv4_write_kernel<<<static_cast<unsigned>(ceil_div(n, kKv4Warps)), 32 * kKv4Warps, 0,
+  kv4_write_kernel<<<static_cast<unsigned>(ceil_div(n, kKv4Warps * kKv4Rows)), 32 * kKv4Warps, 0,
                      reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return launch_check("kv4_write_kernel");
 }
@@ -1262,7 +1331,7 @@ hisa_status hisa_kv4_read(const void* cache, int64_t num_slots, const int32_t* s
   if (e != HISA_OK || n == 0) return e;
   Kv4RowParams p{slots, static_cast<uint8_t*>(const_cast<void*>(cache)), static_cast<uint8_t*>(rows), n, num_slots,
                  row_stride * 2};
-  kv4_read_kernel<<<static_cast<unsigned>(ceil_div(n, kKv4Warps)), 32 * kKv4Warps, 0,
+  kv4_read_kernel<<<static_cast<unsigned>(ceil_div(n, kKv4Warps * kKv4Rows)), 32 * kKv4Warps, 0,
                     reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return launch_check("kv4_read_kernel");
 }

@@ -118,4 +118,220 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) norm_rotary_rows_kernel(con
   for (int j = p.first + lane; j < p.last; j += 32) store_elem<DT>(p.out, oi + j, b[j]);
 }
 
+// ---------------------------------------------------------------- whole vectors
+//
+// Rows of whole 16-byte vectors: G lanes (a power of two) hold a row in
+// registers, V vectors a lane, vector k of the row in lane k mod G.  The kernel
+// moves every byte once each way and is bound by that: MEASURED_ROT
+//   - the angles depend on the token alone: a block of some rows works out the
+//     (cos, sin) of its few tokens once, in shared memory, for all their heads
+//     (the first rows are on their way meanwhile);
+//   - weight and bias of a lane's features stay in registers over its rows
+//     where they are few (two vectors a lane), for the occupancy's sake;
+//   - the partner of a half-layout pair lies rot / 2 features away.  With G as
+//     many vectors as that it is the same lane's next or last vector (PAIRED);
+//     otherwise it is loaded again, from L1.  All loads of a row are made
+//     before its first store, so in place is safe.
+
+template <int DT> __device__ __forceinline__ uint4 pack_vec(const float (&x)[Vec16<DT>::n]);
+template <> __device__ __forceinline__ uint4 pack_vec<DT_F32>(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+template <> __device__ __forceinline__ uint4 pack_vec<DT_BF16>(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT>
+__device__ __forceinline__ void load_features(float (&w)[Vec16<DT>::n], const float* src) {
+#pragma unroll
+  for (int e = 0; e + 4 <= Vec16<DT>::n; e += 4) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(src + e));
+    w[e] = f.x; w[e + 1] = f.y; w[e + 2] = f.z; w[e + 3] = f.w;
+  }
+}
+
+constexpr int kRotaryThreads = 256;
+constexpr int kRotaryTable = 4096;             // (cos, sin) pairs of a block
+
+enum : int { PAIRS_INTERLEAVED, PAIRS_RELOAD, PAIRS_IN_LANE };
+
+// Blocks an SM: enough loads in flight to keep HBM busy.
+constexpr int rotary_blocks(int norm, int v) { return v > 4 ? 2 : v > 2 ? 4 : norm == NORM_NONE ? 6 : 4; }
+
+template <int DT, int NORM, int V, int PAIRS>
+__global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_rotary_vec_kernel(const RotaryParams p, int log_g, int nvec,
+                                                                         int rows_per_block) {
+  constexpr int E = Vec16<DT>::n, ES = Elem<DT>::bytes;
+  constexpr bool kKeep = NORM != NORM_NONE && V <= 2;  // weights in registers
+  extern __shared__ __align__(16) uint8_t rot_smem[];
+  const int half = p.rot / 2;
+  uint64_t* turns = reinterpret_cast<uint64_t*>(rot_smem);
+  float2* cs = reinterpret_cast<float2*>(turns + half);
+  const int tid = threadIdx.x, G = 1 << log_g, lane = tid & (G - 1);
+  const int64_t row_lo = static_cast<int64_t>(blockIdx.x) * rows_per_block;
+  const int nrows = static_cast<int>(min(static_cast<int64_t>(rows_per_block), p.rows - row_lo));
+  const int64_t tok_lo = row_lo / p.heads;
+  const int head_lo = static_cast<int>(row_lo - tok_lo * p.heads);
+  const int ntok = (head_lo + nrows - 1) / p.heads + 1;
+
+  // row r of the block: its vectors, and the partners that other lanes hold
+  uint4 raw[V], mate[PAIRS == PAIRS_RELOAD ? V : 1];
+  bool live = false;
+  int tk = 0;
+  uint8_t* outr = nullptr;
+  auto load = [&](int r) {
+    live = r < nrows;
+    const int at = head_lo + (live ? r : 0);
+    tk = at / p.heads;
+    const int head = at - tk * p.heads;
+    const uint8_t* xr = static_cast<const uint8_t*>(p.x) + ((tok_lo + tk) * p.x_token + head * p.x_head) * ES;
+    outr = static_cast<uint8_t*>(p.out) + ((tok_lo + tk) * p.out_token + head * p.out_head) * ES;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int k = lane + v * G, j = p.first + k * E, jr = j - p.offset;
+      if (!live || k >= nvec) continue;
+      raw[v] = *reinterpret_cast<const uint4*>(xr + j * ES);
+      if (PAIRS == PAIRS_RELOAD && jr >= 0 && jr < p.rot)
+        mate[PAIRS == PAIRS_RELOAD ? v : 0] = *reinterpret_cast<const uint4*>(xr + (jr < half ? j + half : j - half) * ES);
+    }
+  };
+  load(tid >> log_g);
+
+  float w[kKeep ? V : 1][E], b[kKeep && NORM == NORM_LAYER ? V : 1][E];
+  if (kKeep) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int j = (lane + v * G) * E;                // a norm's rows start at feature 0
+      if (j >= p.norm_dim) continue;
+      load_features<DT>(w[v], p.weight + j);
+      if (NORM == NORM_LAYER) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) b[v][e] = 0.f;
+        if (p.bias) load_features<DT>(b[v], p.bias + j);
+      }
+    }
+  }
+  for (int i = tid; i < half; i += kRotaryThreads) turns[i] = turns64(p.inv_freq[i]);
+  __syncthreads();
+  for (int e = tid; e < ntok * half; e += kRotaryThreads) {
+    const int t = e / half;
+    cs[e] = turn_of(__ldg(p.pos + tok_lo + t), turns[e - t * half], p.amplitude, p.sign);
+  }
+  __syncthreads();
+
+  const int step = kRotaryThreads >> log_g;
+  for (int r0 = 0; r0 < nrows; r0 += step) {           // the same trips for a warp's every group: they shuffle together
+    float mean = 0.f, rs = 1.f;
+    if (NORM != NORM_NONE) {
+      const float inv_n = 1.f / static_cast<float>(p.norm_dim);
+      if (NORM == NORM_LAYER) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int k = lane + v * G;
+          if (!live || k >= nvec || k * E >= p.norm_dim) continue;
+          float x[E];
+          Vec16<DT>::unpack(raw[v], x);
+#pragma unroll
+          for (int e = 0; e < E; ++e) mean += x[e];
+        }
+        for (int o = G >> 1; o; o >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+        mean *= inv_n;
+      }
+      float sq = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int k = lane + v * G;
+        if (!live || k >= nvec || k * E >= p.norm_dim) continue;
+        float x[E];
+        Vec16<DT>::unpack(raw[v], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sq += NORM == NORM_LAYER ? (x[e] - mean) * (x[e] - mean) : x[e] * x[e];
+      }
+      for (int o = G >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      rs = 1.f / sqrtf(sq * inv_n + p.eps);
+    }
+    // features j .. j + E - 1 of vector `from`, normed (vector v's own, or its partner's)
+    auto normed = [&](float (&x)[E], const uint4& from, int j, int v, bool own) {
+      Vec16<DT>::unpack(from, x);
+      if (NORM == NORM_NONE || j >= p.norm_dim) return;
+      float wl[E], bl[E];
+      if (kKeep && own) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          wl[e] = w[kKeep ? v : 0][e];
+          if (NORM == NORM_LAYER) bl[e] = b[kKeep && NORM == NORM_LAYER ? v : 0][e];
+        }
+      } else {
+        load_features<DT>(wl, p.weight + j);
+        if (NORM == NORM_LAYER) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) bl[e] = 0.f;
+          if (p.bias) load_features<DT>(bl, p.bias + j);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        x[e] = NORM == NORM_LAYER ? (x[e] - mean) * rs * wl[e] + bl[e] : x[e] * rs * wl[e];
+    };
+    __syncwarp();                                      // every load of the row before its first store
+    const float2* turn = cs + tk * half;
+    if (PAIRS == PAIRS_IN_LANE) {
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        const int k = lane + v * G, j = p.first + k * E, jr = j - p.offset;
+        if (!live || k >= nvec) continue;
+        float x[E], m[E];
+        const bool two = k + G < nvec;
+        normed(x, raw[v], j, v, true);
+        if (two) normed(m, raw[v + 1], j + G * E, v + 1, true);
+        if (jr >= 0 && jr < p.rot) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float2 t = turn[jr + e];
+            const float c = x[e], d = m[e];
+            x[e] = c * t.x - d * t.y;
+            m[e] = d * t.x + c * t.y;
+          }
+        }
+        *reinterpret_cast<uint4*>(outr + j * ES) = pack_vec<DT>(x);
+        if (two) *reinterpret_cast<uint4*>(outr + (j + G * E) * ES) = pack_vec<DT>(m);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int k = lane + v * G, j = p.first + k * E, jr = j - p.offset;
+        if (!live || k >= nvec) continue;
+        float x[E];
+        normed(x, raw[v], j, v, true);
+        if (jr >= 0 && jr < p.rot) {
+          if (PAIRS == PAIRS_INTERLEAVED) {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float2 t = turn[(jr + e) >> 1];
+              const float c = x[e], d = x[e + 1];
+              x[e] = c * t.x - d * t.y;
+              x[e + 1] = d * t.x + c * t.y;
+            }
+          } else {
+            float m[E];
+            const bool low = jr < half;
+            normed(m, mate[PAIRS == PAIRS_RELOAD ? v : 0], low ? j + half : j - half, v, false);
+            const float2* tv = turn + (low ? jr : jr - half);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = x[e] * tv[e].x + m[e] * (low ? -tv[e].y : tv[e].y);
+          }
+        }
+        *reinterpret_cast<uint4*>(outr + j * ES) = pack_vec<DT>(x);
+      }
+    }
+    load(r0 + step + (tid >> log_g));
+  }
+}
+
 }  // namespace hisa
