@@ -1190,6 +1190,7 @@ hisa_status launch_rotary_lanes(const RotaryParams& p, int norm, int v, int log_
     case 2: return launch_rotary_vec<DT, 2, PAIRS>(p, norm, log_g, nvec, st);
     case 3: return launch_rotary_vec<DT, 3, PAIRS>(p, norm, log_g, nvec, st);
     case 4: return launch_rotary_vec<DT, 4, PAIRS>(p, norm, log_g, nvec, st);
+    case 5: return launch_rotary_vec<DT, 5, PAIRS>(p, norm, log_g, nvec, st);
     default: return launch_rotary_vec<DT, 8, PAIRS>(p, norm, log_g, nvec, st);
   }
 }
@@ -1198,7 +1199,7 @@ template <int DT>
 hisa_status launch_rotary_dt(const RotaryParams& p, int norm, cudaStream_t st) {
   const int64_t es = Elem<DT>::bytes;
   auto whole = [&](int64_t n) { return n * es % 16 == 0; };
-  const bool vec = aligned16(p.x) && aligned16(p.out) && (p.rows == p.heads || (whole(p.x_token) && whole(p.out_token))) &&
+  const bool vec = p.heads < 32768 && p.rot > 2 && aligned16(p.x) && aligned16(p.out) && (p.rows == p.heads || (whole(p.x_token) && whole(p.out_token))) &&
                    (p.heads == 1 || (whole(p.x_head) && whole(p.out_head))) && whole(p.first) && whole(p.last) &&
                    whole(p.offset) && whole(p.rot) && (p.interleaved || whole(p.rot / 2)) && kRotaryTable / (p.rot / 2) >= 2 &&
                    (norm == NORM_NONE || (whole(p.norm_dim) && aligned16(p.weight) && aligned16(p.bias)));
@@ -1215,7 +1216,7 @@ hisa_status launch_rotary_dt(const RotaryParams& p, int norm, cudaStream_t st) {
     }
     // vectors a lane: the count that wastes the fewest lanes; of equals one
     // that leaves 8 lanes (128 bytes) a row
-    const int choices[] = {2, 1, 4, 3, 8};
+    const int choices[] = {2, 1, 4, 3, 5, 8};
     int best = 0, best_lg = 0, best_slots = INT32_MAX;
     for (int v : choices) {
       int lg = 0;
@@ -1272,6 +1273,9 @@ hisa_status run_rotary(const void* x, int64_t xt, int64_t xh, const int32_t* pos
   p.last = inplace ? std::max(norm == NORM_NONE ? 0 : norm_dim, offset + rotary_dim) : dim;
   p.amplitude = amplitude; p.eps = eps; p.sign = reverse ? -1.f : 1.f;
   p.interleaved = interleaved != 0;
+  // exact for the vector kernel's n (a block's rows and heads, its table): n * divisor < 2^32
+  p.head_magic = heads == 1 ? 0u : static_cast<uint32_t>((uint64_t(1) << 32) / heads + 1);
+  p.half_magic = static_cast<uint32_t>((uint64_t(1) << 32) / std::max(rotary_dim / 2, 2) + 1);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == HISA_F32 ? launch_rotary_dt<DT_F32>(p, norm, st) : launch_rotary_dt<DT_BF16>(p, norm, st);
 }

@@ -34,6 +34,7 @@ struct RotaryParams {
   int64_t x_token, x_head, out_token, out_head;   // strides in elements
   int64_t rows;              // tokens * heads
   int heads, dim, rot, offset, norm_dim;
+  uint32_t head_magic, half_magic;   // n / heads, n / (rot / 2) as the upper half of n * magic, for n below 2^32 / divisor
   int first, last;           // features [first, last) are written
   float amplitude, eps, sign;   // sign: -1 turns back
   bool interleaved;
@@ -162,7 +163,7 @@ constexpr int kRotaryTable = 4096;             // (cos, sin) pairs of a block
 enum : int { PAIRS_INTERLEAVED, PAIRS_RELOAD, PAIRS_IN_LANE };
 
 // Blocks an SM: enough loads in flight to keep HBM busy.
-constexpr int rotary_blocks(int norm, int v) { return v > 4 ? 2 : v > 2 ? 4 : norm == NORM_NONE ? 6 : 4; }
+constexpr int rotary_blocks(int norm, int v) { return v > 5 ? 2 : v > 4 ? 3 : v > 2 ? 4 : norm == NORM_NONE ? 6 : 4; }
 
 template <int DT, int NORM, int V, int PAIRS>
 __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_rotary_vec_kernel(const RotaryParams p, int log_g, int nvec,
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
   auto load = [&](int r) {
     live = r < nrows;
     const int at = head_lo + (live ? r : 0);
-    tk = at / p.heads;
+    tk = p.heads == 1 ? at : static_cast<int>(__umulhi(static_cast<uint32_t>(at), p.head_magic));
     const int head = at - tk * p.heads;
     const uint8_t* xr = static_cast<const uint8_t*>(p.x) + ((tok_lo + tk) * p.x_token + head * p.x_head) * ES;
     outr = static_cast<uint8_t*>(p.out) + ((tok_lo + tk) * p.out_token + head * p.out_head) * ES;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
   for (int i = tid; i < half; i += kRotaryThreads) turns[i] = turns64(p.inv_freq[i]);
   __syncthreads();
   for (int e = tid; e < ntok * half; e += kRotaryThreads) {
-    const int t = e / half;
+    const int t = static_cast<int>(__umulhi(static_cast<uint32_t>(e), p.half_magic));
     cs[e] = turn_of(__ldg(p.pos + tok_lo + t), turns[e - t * half], p.amplitude, p.sign);
   }
   __syncthreads();
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
         for (int e = 0; e < E; ++e) sq += NORM == NORM_LAYER ? (x[e] - mean) * (x[e] - mean) : x[e] * x[e];
       }
       for (int o = G >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      rs = 1.f / sqrtf(sq * inv_n + p.eps);
+      rs = rsqrtf(sq * inv_n + p.eps);
     }
     // features j .. j + E - 1 of vector `from`, normed (vector v's own, or its partner's)
     auto normed = [&](float (&x)[E], const uint4& from, int j, int v, bool own) {
