@@ -781,11 +781,12 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
         float mx4[4] = {-kInf, -kInf, -kInf, -kInf};
 #pragma unroll
         for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], s[i]);
-        const float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+        float mt = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
         // the reference: the maximum of the query's first 32 keys, handed to
         // the other group and both of the peer's; it stays unless exceeded by 2^64
         if (k == 0) {
           if (rank == 0 && g == 0) {
+            mt = fmaxf(mt, -3e38f);                    // 32 logits of -inf: weights of 0, not of exp2(-inf + inf)
             m_first = mt;
             if (it.tiles > 1)
               st_async_b32(peer_addr(&sm->m_first[par][h], peer), mt, peer_addr(&sm->first_full[par], peer));
@@ -938,7 +939,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
         mbar_arrive_remote(peer_fin_free);
       }
       tc_fence_after();
-      const float inv = 1.f / l;
+      const float inv = l != 0.f ? 1.f / l : 0.f;      // every logit -inf: as an empty set
 #pragma unroll 1
       for (int c0 = 0; c0 < 256; c0 += 32) {
         uint32_t x[32];

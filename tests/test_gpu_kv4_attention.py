@@ -244,6 +244,35 @@ def test_masked_places_may_hold_anything(lib):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_logits_that_are_not_finite(lib):
+    """A positional feature of -inf (in the query's sign, so a logit of -inf) takes
+    its key's weight away, be it a whole tile's, the first 32 keys' or all keys';
+    NaN and +inf make their query NaN and no other."""
+    L = 400
+    c = Case(1, L, 64, 17)
+    q = _q(1, 4, 128, 17)
+    q[..., 512] = q[..., 512].abs() + 0.5
+    idx = np.tile(np.arange(200, dtype=np.int32), (1, 4, 1))
+    idx[0, 1] += 100
+    idx[0, 3] += 200
+    want = idx.copy()
+    gone = list(range(0, 40)) + list(range(128, 192)) + list(range(200, 400))
+    for s in gone:
+        row = c.kv[0, s].copy()
+        row[512] = -np.inf
+        t = torch.from_numpy(row).to(torch.bfloat16).view(1, 576).cuda()
+        _hb().hisa_kv4_write(t, c.slots[0, s].view(1).cuda(), c.cache)
+    want[np.isin(want, gone)] = -1
+    o, lse = c.run(q, idx)
+    c.check(q, want, o, lse, "-inf")                       # query 3: an empty set
+    bad = torch.from_numpy(c.kv[0, 60:61]).to(torch.bfloat16).cuda()
+    bad[0, 520] = float("nan")
+    _hb().hisa_kv4_write(bad, c.slots[0, 60].view(1).cuda(), c.cache)
+    o2, lse2 = c.run(q, idx)
+    assert o2[0, [0, 2]].isnan().all() and lse2[0, [0, 2]].isnan().all()
+    assert torch.equal(o2[0, [1, 3]], o[0, [1, 3]]) and torch.equal(lse2[0, [1, 3]], lse[0, [1, 3]])
+
+
 def test_streams_and_graphs(lib):
     """Two captured calls of different sizes, replayed in either order, and a call on another stream."""
     hb = _hb()
