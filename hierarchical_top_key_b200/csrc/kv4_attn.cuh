@@ -17,15 +17,26 @@
 //    softmax weights P, and puts P (bf16, 16 KB) into its own shared memory
 //    and its peer's; both add P . V for their half of the features.  Nothing
 //    is computed twice, and what crosses between the SMs is 8 KB a tile each
-//    way (exchanging fp32 partial logits instead takes 32 KB, and the writes
-//    into the peer's memory then hold up every other shared-memory access).
-//    Eight producer warps load the records' codes, turn them into bf16 in
+//    way.  Producer warps load the records' codes, turn them into bf16 in
 //    registers and store them in the swizzled layout the MMA reads: 4-bit rows
 //    cross L2 and HBM, bf16 rows exist only in shared memory.  An owned tile
 //    needs the whole row, the peer's tile only this CTA's value half.
 // 3. Few queries are split over the keys: part i of a row takes a contiguous
 //    run of its tiles and writes an fp32 output with its own lse;
 //    kv4_join_kernel joins the parts.
+//
+// Measured (128 heads, 2048 keys of 64K, 1024 queries): 0.70 ms = 835 TFLOP/s,
+// half the measured bf16 burst rate; the bf16 kernel of sparse_attn.cuh takes
+// 1.02 ms.  Other divisions of the work, as whole kernels: features split and
+// fp32 partial logits exchanged (32 KB a tile each way) 1.08 ms; the logits
+// computed by both CTAs, nothing exchanged, 0.97 ms (shared memory's data path
+// is then busy 98 % of the time).  What bounds it now is the life of a tile's
+// buffers: 227 KB hold two own tiles' value halves but one of the rest of a row
+// and one of the peer's, so a tile's chain (keys 2K cycles, logit MMAs 1.3K,
+// softmax 2.7K, output MMA 0.5K) overlaps the next one's only in part: 4.6K
+// cycles a pair of tiles, 2.4K of them MMA.  Tried without gain: 4 or 8 warps
+// on the own tiles' halves, row loads 64 bytes a lane pair, the shifts of the
+// decoding as multiplications, the weights to the own memory first.
 //
 // Softmax reference.  P of a tile is exp2(logit - m) for a reference m per head
 // row that need not be the maximum: fp32 sums and bf16 weights keep their
