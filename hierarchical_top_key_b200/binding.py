@@ -510,6 +510,8 @@ def _rotary(name, x, positions, inv_freq, offset, out, weight=None, bias=None):
         if out.shape != x.shape or out.dtype != x.dtype:
             raise ValueError("out must have x's shape and dtype")
         _, _, _, ots, ohs = _rows_of(out, "out")
+    if not 0 <= offset <= dim:
+        raise ValueError(f"offset must be in [0, {dim}], got {offset}")
     _on(x.get_device(), name, positions, inv_freq, out, weight, bias)
     return tokens, heads, dim, ts, hs, out, ots, ohs
 
@@ -609,6 +611,10 @@ def hisa_sparse_attention_kv4(q, cache, page_table, idx, *, scale: float, num_ke
         raise TypeError(f"q must be bfloat16 [batch, Q, H, {KV4_WIDTH}]")
     if idx.dtype != torch.int32 or idx.shape[:2] != (b, Q):
         raise ValueError("idx must be int32 [batch, Q, top_k]")
+    if not 1 <= num_keys < 2 ** 31:
+        raise ValueError(f"num_keys must be in [1, 2^31), got {num_keys}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     pages = -(-num_keys // cache.shape[1])
     if page_table.dtype != torch.int32 or tuple(page_table.shape) != (b, pages):
         raise ValueError(f"page_table must be int32 {(b, pages)}, got {page_table.dtype} {tuple(page_table.shape)}")

@@ -355,6 +355,21 @@ __device__ __forceinline__ uint64_t desc_k_none(uint32_t smem_addr, uint32_t lbo
 
 // ---------------------------------------------------------------- work items
 
+// A load that stays where it is written: the compiler moves plain ones down to
+// their use, and the latency with them.  For what the selection wrote, which
+// may still have been writing when this kernel started; ldg32_here for what no
+// kernel in flight writes.
+__device__ __forceinline__ uint32_t ld32_here(const void* src) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(src));
+  return v;
+}
+__device__ __forceinline__ uint32_t ldg32_here(const void* src) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(src));
+  return v;
+}
+
 // A work item, one (query, head slice, part): its tiles are t = 0 .. tiles-1,
 // those with t & 1 == rank are this CTA's own.  The part's keys are list[first
 // .. first + n).
@@ -365,7 +380,7 @@ struct Kv4Item {
     part = static_cast<int>(item % p.parts);
     slice = static_cast<int>(item / p.parts % p.slices);
     row = item / p.parts / p.slices;
-    const int n_row = __ldg(p.count + row);
+    const int n_row = static_cast<int>(ld32_here(p.count + row));
     const int t_row = (n_row + kAttnTileN - 1) / kAttnTileN;
     const int t0 = static_cast<int>(static_cast<int64_t>(t_row) * part / p.parts);
     tiles = static_cast<int>(static_cast<int64_t>(t_row) * (part + 1) / p.parts) - t0;
@@ -387,14 +402,6 @@ __device__ __forceinline__ void ldg256(uint32_t (&w)[8], const uint8_t* src) {
   asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(src));
-}
-
-// A load that stays where it is written: the compiler moves plain ones down to
-// their use, and the latency with them.
-__device__ __forceinline__ uint32_t ldg32_here(const void* src) {
-  uint32_t v;
-  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(src));
-  return v;
 }
 
 __device__ __forceinline__ void kv4_load_piece(Kv4Piece& k, const uint8_t* rec, int panel) {
@@ -702,7 +709,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
       const int32_t* list = p.list + it.row * p.list_ld + it.first;
       // the record of the tile's row rr; past the last key that key's again, masked by the softmax
       int row0 = static_cast<int>(kind) * kAttnTileN + r;
-      auto record = [&](int rr) -> uint32_t { return ldg32_here(list + min(row0 + rr, it.n - 1)); };
+      auto record = [&](int rr) -> uint32_t { return ld32_here(list + min(row0 + rr, it.n - 1)); };
       Kv4Piece a, b;
       uint32_t ra[8], rb[8];                           // team 2: 16 of each row's 64 positional features
       uint32_t ida = record(0), idb = record(8);

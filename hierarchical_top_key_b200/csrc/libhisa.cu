@@ -1147,9 +1147,15 @@ hisa_status check_rows(const void* x, int64_t xt, int64_t xh, const void* out, i
   if (tokens < 0 || heads < 1 || dim < 1) return fail(HISA_ERR_INVALID_ARG, "tokens must be >= 0, heads and dim >= 1");
   if (dim > kRotaryMaxDim) return fail(HISA_ERR_UNSUPPORTED, "dim must be <= %d", kRotaryMaxDim);
   if (xt < 0 || xh < 0 || ot < 0 || oh < 0) return fail(HISA_ERR_INVALID_ARG, "strides must be >= 0");
-  // a row of out written by two (token, head) pairs would be a race
-  if ((tokens > 1 && ot < dim) || (heads > 1 && oh < dim))
-    return fail(HISA_ERR_INVALID_ARG, "out's rows overlap: its token and head strides must be >= dim");
+  if (tokens > INT64_MAX / heads) return fail(HISA_ERR_UNSUPPORTED, "too many rows");
+  // an element of out that two (token, head) pairs write would be a race: the
+  // rows of one axis lie clear of each other, and so does all that one step of
+  // the other axis holds
+  const __int128 heads_span = static_cast<__int128>(heads - 1) * oh + dim;
+  const __int128 tokens_span = static_cast<__int128>(tokens > 0 ? tokens - 1 : 0) * ot + dim;
+  if ((tokens > 1 && ot < dim) || (heads > 1 && oh < dim) ||
+      (tokens > 1 && heads > 1 && ot < heads_span && oh < tokens_span))
+    return fail(HISA_ERR_INVALID_ARG, "out's rows overlap: its token and head strides must keep them apart");
   if (x == out && tokens > 0 && ((tokens > 1 && xt != ot) || (heads > 1 && xh != oh)))
     return fail(HISA_ERR_INVALID_ARG, "in place, out's strides must be x's");
   return HISA_OK;

@@ -424,9 +424,11 @@ HISA_API hisa_status hisa_sparse_attention(const void* q, const void* kv, const 
  *              contiguous, the other strides given in elements
  *   positions  [tokens] int32;  inv_freq [rotary_dim / 2] fp64 (radians per
  *              position), both device
- *   out        [tokens, heads, dim] likewise; x itself with x's strides (only
- *              the turned features are then touched), else no element of out
- *              may be one of x
+ *   out        [tokens, heads, dim] likewise, no element of it in two rows: the
+ *              stride of one axis is at least dim, that of the other at least
+ *              all that the first spans; x itself with x's strides (only the
+ *              turned features are then touched), else no element of out may
+ *              be one of x
  * Pointers are aligned to their element size (inv_freq 8, positions 4 bytes);
  * 16-byte aligned rows run faster.  dim <= 1024, rotary_dim even and >= 2.
  * tokens == 0 returns HISA_OK without a launch.

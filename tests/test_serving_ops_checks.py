@@ -46,6 +46,19 @@ def test_rotary_arguments(L, kw, status):
     assert _rot(L, **kw) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(heads=2, ot=128, oh=128),                  # token 1's head 0 is token 0's head 1
+    dict(heads=3, ot=192, oh=128), dict(heads=2, tokens=3, ot=128, oh=256),
+    dict(heads=4, tokens=2, ot=511, oh=128)])
+def test_rotary_refuses_rows_of_out_that_overlap(L, kw):
+    assert _rot(L, **kw) == 1 and _norm(L, **kw) == 1
+
+
+def test_rotary_refuses_more_rows_than_it_can_count(L):
+    assert _rot(L, heads=4, tokens=1 << 62, ot=1 << 20) == 2
+    assert _rot(L, heads=2, tokens=1 << 62, ot=1 << 62, oh=1 << 62, rot=63) == 2     # 2^63 rows
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(norm=0), 1), (dict(norm=3), 1), (dict(nd=0), 1), (dict(nd=129), 1), (dict(b=0x5000), 1),
     (dict(w=None), 1), (dict(eps=f32(-1.0)), 1), (dict(eps=f32(float("inf"))), 1), (dict(w=0x4002), 1),
