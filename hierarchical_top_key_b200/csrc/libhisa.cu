@@ -1165,10 +1165,15 @@ bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) &
 
 template <int DT, int V, int PAIRS>
 hisa_status launch_rotary_vec(const RotaryParams& p, int norm, int log_g, int nvec, cudaStream_t st) {
-  // some rows a lane group, as few as still fill the SMs; at most as many
-  // tokens as the block's table of turns holds
+  // rows a lane group: up to 6 (fewer: the block's turns cost more than the rows
+  // hide; 12: 2 % slower), and such that the blocks fill their last wave: 164K
+  // fp32 rows with a norm take 34.8 us so, 38.9 with 8 rows in 2.2 waves, 32K
+  // rows of 576 22.6 with 5 in one wave, 24.6 with 6 or 2.  At most as many
+  // tokens as the block's table of turns holds.
   const int groups = kRotaryThreads >> log_g, half = p.rot / 2;
-  const int64_t per = std::min<int64_t>(8, std::max<int64_t>(1, p.rows / (static_cast<int64_t>(groups) * num_sms() * 8)));
+  const int64_t wave = static_cast<int64_t>(groups) * num_sms() * rotary_blocks(norm, V);
+  const int64_t waves = ceil_div(ceil_div(p.rows, wave), 6);
+  const int64_t per = ceil_div(p.rows, wave * waves);
   const int64_t max_tokens = kRotaryTable / half;
   const int64_t rows = std::min(groups * per, p.heads == 1 ? max_tokens : (max_tokens - 1) * p.heads);
   const int64_t blocks = ceil_div(p.rows, rows);

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) norm_rotary_rows_kernel(con
 // moves every byte once each way: 64 heads of 128, 32K tokens, bf16, out of
 // place, take 167 us (6.4 TB/s, 0.98 of the measured copy bandwidth; the row
 // kernel above 588).  With a norm the instructions a row cost show: 32K rows of
-// 576 (bf16) 24.6 us = 3.1 TB/s, 164K fp32 rows of 128 38.9 us = 4.3 TB/s.
+// 576 (bf16) 22.6 us = 3.3 TB/s, 164K fp32 rows of 128 34.9 us = 4.8 TB/s.
 //   - the angles depend on the token alone: a block of some rows works out the
 //     (cos, sin) of its few tokens once, in shared memory, for all their heads
 //     (the first rows are on their way meanwhile);
