@@ -25,7 +25,7 @@
 //    run of its tiles and writes an fp32 output with its own lse;
 //    kv4_join_kernel joins the parts.
 //
-// Measured (128 heads, 2048 keys of 64K, 1024 queries): 0.70 ms = 835 TFLOP/s,
+// Measured (128 heads, 2048 keys of 64K, 1024 queries): 0.69 ms = 851 TFLOP/s,
 // half the measured bf16 burst rate; the bf16 kernel of sparse_attn.cuh takes
 // 1.02 ms.  Other divisions of the work, as whole kernels: features split and
 // fp32 partial logits exchanged (32 KB a tile each way) 1.08 ms; the logits
@@ -50,12 +50,12 @@
 // Warp roles (26 warps a CTA, a persistent pair over queries):
 //   warp 0       TMEM owner, logit MMA issuer (one thread)
 //   warp 1       output MMA issuer (one thread)
-//   warps 2..13  producers, three teams of four: the query, and the value
-//                half of the peer's tiles; the value half of the own tiles;
-//                the rest of the own tiles
+//   warps 2..13  producers, three teams of four: the value half of the
+//                peer's tiles; the value half of the own tiles; the rest of
+//                the own tiles
 //   warps 14..21 softmax of the own tiles: group g has keys 32g .. 32g+31, a
 //                thread a head row
-//   warps 22..25 the output, and the scaling above
+//   warps 22..25 the next query, the output, and the scaling above
 // Own tiles are numbered u, the peer's v, through all of a pair's queries.
 // Every wait is bounded; a timeout sets the CTA's abort flag and the status
 // word, and the peer CTA's waits on it then time out too.
@@ -72,8 +72,9 @@ struct Kv4AttnParams {
   int Q, L, heads, top_k, list_ld;
   int page_size, page_shift, pages_per_seq, num_pages;   // page_shift: log2(page_size), or -1
   int slices, parts;         // slices of 128 heads; parts of a row's keys
+  int64_t rows;              // (query, head) pairs of q
   int64_t row0;              // the first query of this launch (of the chunk its workspace holds)
-  int64_t items;             // (queries of this launch) * slices * parts
+  uint32_t items;            // (queries of this launch) * slices * parts
   float scale_log2;          // |softmax scale| * log2(e), 1 for a scale of 0
   int sign;                  // of the scale: the logits are multiplied by it unless it is 1
   const int32_t* idx;        // [rows, top_k]
@@ -233,6 +234,7 @@ constexpr uint32_t kKv4Kx = 5 * kKv4Panel;                // an owned tile's oth
 constexpr uint32_t kKv4P = kAttnHeads * kAttnTileN * 2;   // a tile's weights
 
 struct Kv4Smem {
+  uint64_t q_in[4][3];                         // [output warp][panel slot]: its 32 rows of a panel of the query
   uint64_t q_full, q_free, o_empty;            // a query is in place; its last own logits are done; its output has been read
   uint64_t kx_full, kx_empty, vo_full[2], vo_empty[2];   // own tiles (kx: the rest of a row)
   uint64_t vr_full, vr_empty;                  // the peer's tiles
@@ -277,16 +279,24 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Whether the phase has completed.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(sm100::smem_u32(bar)), "r"(phase & 1)
+               : "memory");
+  return ok != 0;
+}
 // Arrive on a barrier of another CTA of the cluster (a cluster address).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// 16 bytes into shared memory on their own, zeros unless `valid`.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// `bytes` (a multiple of 16) at the 16-byte aligned `src` towards L2.
+__device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void stg256(void* dst, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
@@ -376,19 +386,39 @@ __device__ __forceinline__ uint32_t ldg32_here(const void* src) {
 struct Kv4Item {
   int64_t row;               // within this launch
   int slice, part, tiles, first, n;
-  __device__ __forceinline__ Kv4Item(const Kv4AttnParams& p, int64_t item) {
-    part = static_cast<int>(item % p.parts);
-    slice = static_cast<int>(item / p.parts % p.slices);
-    row = item / p.parts / p.slices;
-    const int n_row = static_cast<int>(ld32_here(p.count + row));
-    const int t_row = (n_row + kAttnTileN - 1) / kAttnTileN;
-    const int t0 = static_cast<int>(static_cast<int64_t>(t_row) * part / p.parts);
-    tiles = static_cast<int>(static_cast<int64_t>(t_row) * (part + 1) / p.parts) - t0;
-    first = t0 * kAttnTileN;
-    n = min(n_row - first, tiles * kAttnTileN);
-  }
   __device__ __forceinline__ int own(uint32_t rank) const { return (tiles + 1 - static_cast<int>(rank)) >> 1; }
   __device__ __forceinline__ int keys_of(int t) const { return min(kAttnTileN, n - t * kAttnTileN); }
+};
+
+// A pair's items in turn, every role for itself; the next row's number of
+// records is on its way while an item is worked on.
+struct Kv4Walk {
+  const Kv4AttnParams& p;
+  uint32_t at, step;
+  int count;
+  __device__ __forceinline__ explicit Kv4Walk(const Kv4AttnParams& params)
+      : p(params), at(sm100::cluster_id_x()), step(gridDim.x / 2) {
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    count = at < p.items ? static_cast<int>(ld32_here(p.count + at / static_cast<uint32_t>(p.slices * p.parts))) : 0;
+  }
+  __device__ __forceinline__ bool next(Kv4Item& it) {
+    if (at >= p.items) return false;
+    const uint32_t parts = static_cast<uint32_t>(p.parts), slices = static_cast<uint32_t>(p.slices);
+    const uint32_t rest = at / parts;
+    it.part = static_cast<int>(at - rest * parts);
+    it.row = rest / slices;
+    it.slice = static_cast<int>(rest - static_cast<uint32_t>(it.row) * slices);
+    const int t_row = (count + kAttnTileN - 1) / kAttnTileN;           // at most 64, as parts
+    const int t0 = t_row * it.part / p.parts;
+    it.tiles = t_row * (it.part + 1) / p.parts - t0;
+    it.first = t0 * kAttnTileN;
+    it.n = min(count - it.first, it.tiles * kAttnTileN);
+    at += step;
+    fetch();
+    return true;
+  }
 };
 
 // Half of a record's codes for one tile row and panel (64 codes and their four
@@ -440,7 +470,8 @@ __device__ __forceinline__ void kv4_store_piece(const Kv4Piece& k, uint32_t row_
 
 // ---------------------------------------------------------------- the kernel
 
-__global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnParams p,
+                                                                   const __grid_constant__ CUtensorMap qmap) {
   using namespace sm100;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Kv4Smem* sm = reinterpret_cast<Kv4Smem*>(smem_raw);
@@ -459,12 +490,12 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
-  const int64_t item0 = cluster_id_x(), step = gridDim.x / 2;
   // bytes that the peer's softmax sends with a tile (weights, references, the
   // warps' marks) and with a query (sums and references)
   constexpr uint32_t kPBytes = kKv4P + 2 * kAttnHeads * 4 + 8 * 4, kFinBytes = 4 * kAttnHeads * 4;
 
   if (tid == 0) {
+    for (int i = 0; i < 12; ++i) mbar_init(&sm->q_in[i / 3][i % 3], 1);
     mbar_init(&sm->q_full, 4);
     mbar_init(&sm->q_free, 1);
     mbar_init(&sm->o_empty, 4);
@@ -494,11 +525,10 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(&sm->tmem_base, 512);
-  if (tid >= kKv4CorrBase) {                           // the first query towards L2
-    const int slice = static_cast<int>(item0 / p.parts % p.slices), h = slice * kAttnHeads + tid - kKv4CorrBase;
-    const uint16_t* qh = p.q + ((p.row0 + item0 / p.parts / p.slices) * p.heads + h) * kAttnDqk;
+  if (tid >= kKv4CorrBase && lane == 0) {              // the first query towards L2
+    const int rest = static_cast<int>(cluster_id_x()) / p.parts, h = rest % p.slices * kAttnHeads + (warp & 3) * 32;
     if (h < p.heads)
-      for (int i = 0; i < 9; ++i) prefetch_l2(qh + 64 * i);
+      prefetch_l2_bulk(p.q + ((p.row0 + rest / p.slices) * p.heads + h) * kAttnDqk, min(32, p.heads - h) * kAttnDqk * 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -513,6 +543,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
   auto wait_peer = [&](uint64_t* bar, uint32_t phase) -> bool {   // completed by the other CTA
     return __all_sync(kFull, mbar_wait_cluster(bar, phase & 1, abort_flag));
   };
+  Kv4Walk walk(p);
+  Kv4Item it;
   auto warp_arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -527,8 +559,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
       const uint64_t q_desc = desc_k_sw128(smem_u32(q_buf)), kx_desc = desc_k_sw128(smem_u32(kx_buf));
       uint32_t u = 0, live = 0;
       bool ok = true;
-      for (int64_t item = item0; ok && item < p.items; item += step) {
-        const int own = Kv4Item(p, item).own(rank);
+      while (ok && walk.next(it)) {
+        const int own = it.own(rank);
         if (own == 0) continue;
         if (!(ok = mbar_wait(&sm->q_full, live & 1, abort_flag))) break;
         ++live;
@@ -581,8 +613,8 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
       uint32_t u = 0, v = 0, live = 0, fixes = 0, drains = 0;
       bool ok = true;
       mbar_arrive_expect_tx(&sm->p_peer, kPBytes);     // the first of the peer's weights
-      for (int64_t item = item0; ok && item < p.items; item += step) {
-        const int tiles = Kv4Item(p, item).tiles;
+      while (ok && walk.next(it)) {
+        const int tiles = it.tiles;
         if (tiles == 0) continue;
         // the previous query's output has been read
         if (live > 0 && !(ok = mbar_wait(&sm->o_empty, (live - 1) & 1, abort_flag))) break;
@@ -646,64 +678,16 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     // stored, with record numbers looked up one tile before that.
     // One code for the three teams (three copies of it, and instruction
     // fetches hold up every warp).
-    const int pw = warp - kKv4ProdBase / 32, team = pw >> 2;     // 0: query, peer's values; 1: own values; 2: own rest
+    const int pw = warp - kKv4ProdBase / 32, team = pw >> 2;     // 0: peer's values; 1: own values; 2: own rest
     const int panel = lane & 3;
     const int r = (pw & 3) * 16 + (lane >> 2);         // and r + 8
     const uint32_t kind = team == 0 ? peer : rank;     // parity of the team's tiles
     const uint32_t code_panel = 4 * (team == 2 ? peer : rank) + panel;     // of a record
     const uint32_t out_at = smem_u32(team == 0 ? vr_buf : team == 1 ? vo_buf : kx_buf) + panel * kKv4Panel + r * 128;
     const uint32_t rope_at = smem_u32(kx_buf) + 4 * kKv4Panel + ((r * 128) | (((2 * panel) ^ (r & 7)) << 4));
-    uint32_t n = 0, loaded = 0;                        // tiles made, queries loaded, through all queries
+    uint32_t n = 0;                                    // tiles made, through all queries
     bool ok = true;
-    for (int64_t item = item0; ok && item < p.items; item += step) {
-      const Kv4Item it(p, item);
-      if (team == 0 && it.own(rank) > 0) {
-        // the query's rows, behind the last own logits of the one before:
-        // three panels at a time into shared memory (eight lanes a row: a line
-        // a row and panel), the first six from there into TMEM
-        const int quarter = warp & 3, h = quarter * 32 + lane;
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint16_t* qs = p.q + ((p.row0 + it.row) * p.heads + it.slice * kAttnHeads) * kAttnDqk;
-        const int heads = min(kAttnHeads, p.heads - it.slice * kAttnHeads);
-        if (h < heads)                                 // towards L2 until then
-#pragma unroll
-          for (int i = 0; i < 9; ++i) prefetch_l2(qs + h * kAttnDqk + 64 * i);
-        if (loaded > 0 && !(ok = wait(&sm->q_free, loaded - 1))) break;
-        ++loaded;
-        tc_fence_after();
-#pragma unroll 1
-        for (int p0 = 0; p0 < 9; p0 += 3) {
-          // a warp's rows are its own: no other warp reads or writes them
-#pragma unroll 1
-          for (int pn = 0; pn < 3; ++pn) {
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-              const int hr = quarter * 32 + i * 4 + (lane >> 3), c = lane & 7;
-              const bool ok_row = hr < heads;
-              cp_async16(smem_u32(q_buf) + pn * kKv4QPanel + hr * 128 + ((c ^ (hr & 7)) << 4),
-                         qs + (ok_row ? hr : 0) * kAttnDqk + (p0 + pn) * 64 + c * 8, ok_row);
-            }
-          }
-          cp_async_wait_all();
-          __syncwarp();
-          if (p0 + 3 > kKv4QPanels) break;
-#pragma unroll 1
-          for (int pn = 0; pn < 6; ++pn) {             // half panels
-            uint32_t x[16];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 y = lds128(smem_u32(q_buf) + (pn >> 1) * kKv4QPanel + h * 128 + ((((pn & 1) * 4 + i) ^ (h & 7)) << 4));
-              x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
-            }
-            tmem_st16(t_lane + kKv4TmemQ + p0 * 32 + pn * 16, x);
-          }
-          __syncwarp();
-        }
-        tmem_wait_st();
-        fence_proxy_async_smem();
-        tc_fence_before();
-        warp_arrive(&sm->q_full);
-      }
+    while (ok && walk.next(it)) {
       const int mine = it.own(kind);
       if (mine == 0) continue;
       const int32_t* list = p.list + it.row * p.list_ld + it.first;
@@ -767,8 +751,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     uint32_t u = 0, live = 0;
     uint32_t first_phase[2] = {0, 0};
     bool ok = true;
-    for (int64_t item = item0; ok && item < p.items; item += step) {
-      const Kv4Item it(p, item);
+    while (ok && walk.next(it)) {
       if (it.tiles == 0) continue;
       const int own = it.own(rank);
       const uint32_t par = live & 1;
@@ -876,11 +859,79 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     const float kInf = __int_as_float(0x7f800000);
     const uint32_t peer_fin_free = peer_addr(&sm->fin_free, peer);
     if (h == 0) mbar_arrive_expect_tx(&sm->fin_peer, kFinBytes);      // the first of the peer's sums
-    uint32_t live = 0, commands = 0;
-
+    uint32_t live = 0, commands = 0, loaded = 0;       // queries put out, commands, queries loaded
     bool ok = true;
-    for (int64_t item = item0; ok && item < p.items; item += step) {
-      const Kv4Item it(p, item);
+
+    // The next query this CTA has tiles of its own for: one walk ahead.  Its
+    // rows move towards L2 when it becomes the next.
+    if (lane == 0) tma_prefetch_desc(&qmap);
+    Kv4Walk ahead(p);
+    Kv4Item next;
+    bool waiting = false;
+    int q_row = 0;                                     // of the warp's 32 rows; past the end, zeros, for heads past the last
+    auto find_query = [&]() {
+      while ((waiting = ahead.next(next)) && next.own(rank) == 0) {}
+      if (!waiting) return;
+      const int h0 = next.slice * kAttnHeads + quarter * 32;
+      const int64_t row = (p.row0 + next.row) * p.heads + h0;
+      q_row = static_cast<int>(h0 < p.heads ? row : p.rows);
+      if (lane == 0 && h0 < p.heads) prefetch_l2_bulk(p.q + row * kAttnDqk, min(32, p.heads - h0) * kAttnDqk * 2);
+    };
+    // Panel pn of the warp's 32 rows into shared memory; no other warp reads or
+    // writes them.  (Rows past the last head may be the next query's: their
+    // results go nowhere.)
+    auto query_panel = [&](int pn) {
+      if (lane != 0) return;
+      uint64_t* bar = &sm->q_in[quarter][pn % 3];
+      mbar_arrive_expect_tx(bar, 32 * 128);
+      tma_load_2d(q_buf + pn % 3 * kKv4QPanel + quarter * 32 * 128, &qmap, bar, pn * 64, q_row);
+    };
+    auto panel_here = [&](int pn) {                    // after an abort too: the copy is not left in flight
+      uint64_t* bar = &sm->q_in[quarter][pn % 3];
+      const uint32_t parity = (3 * loaded + pn / 3) & 1;
+      if (!mbar_wait(bar, parity, abort_flag)) mbar_drain(bar, parity);
+      __syncwarp();
+    };
+    // The query's rows, behind the last own logits of the one before: the first
+    // six panels go on into TMEM, three in flight, the last three stay.
+    auto load_query = [&]() {
+      tc_fence_after();
+      for (int pn = 0; pn < 3; ++pn) query_panel(pn);
+#pragma unroll 1
+      for (int pn = 0; pn < kKv4QPanels; ++pn) {
+        panel_here(pn);
+        const uint32_t row_at = smem_u32(q_buf) + pn % 3 * kKv4QPanel + h * 128;
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 y = lds128(row_at + ((i ^ (h & 7)) << 4));
+          x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+        }
+        tmem_st32(t_lane + kKv4TmemQ + pn * 32, x);
+        __syncwarp();
+        query_panel(pn + 3);
+      }
+#pragma unroll 1
+      for (int pn = kKv4QPanels; pn < 9; ++pn) panel_here(pn);
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      warp_arrive(&sm->q_full);
+      ++loaded;
+      find_query();
+    };
+    find_query();
+    auto timed_out = [&](uint64_t t0) -> bool {        // or the CTA is aborting, warp-uniform
+      bool out = *abort_flag != 0;
+      if (!out && globaltimer() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        record_status(HISA_ERR_TIMEOUT);
+        out = true;
+      }
+      return __any_sync(kFull, out);
+    };
+
+    while (ok && walk.next(it)) {
       const bool head_ok = it.slice * kAttnHeads + h < p.heads;
       const int64_t orow = it.row * p.heads + it.slice * kAttnHeads + h;      // within this launch
       uint16_t* out = p.o + (p.row0 * p.heads + orow) * kAttnDv + rank * 256;
@@ -897,8 +948,29 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
       }
       bool scaled = false;
       float mo = 0.f;                                  // what the output rows are relative to, once `scaled`
+      uint64_t t0 = globaltimer();
       while (true) {
-        if (!(ok = wait(&sm->ctl, commands))) break;
+        // the next query as soon as its place is free: the output's rest is
+        // then made while its first logits are.  A command may come first, and
+        // may be what that place waits for.
+        if (waiting) {
+          bool command_here, free_here;
+          for (int k = 0;; ++k) {
+            command_here = __all_sync(kFull, mbar_test(&sm->ctl, commands));
+            free_here = __all_sync(kFull, loaded == 0 || mbar_test(&sm->q_free, loaded - 1));
+            if (command_here || free_here || ((k & 63) == 63 && !(ok = !timed_out(t0)))) break;
+            __nanosleep(400);
+          }
+          if (!ok) break;
+          if (!command_here) {
+            load_query();
+            t0 = globaltimer();
+            continue;
+          }
+        } else if (!(ok = wait(&sm->ctl, commands))) {
+          break;
+        }
+        t0 = globaltimer();
         ++commands;
         const int command = *reinterpret_cast<volatile int*>(&sm->command);
         if (command == kKv4Done) break;

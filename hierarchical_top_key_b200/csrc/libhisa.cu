@@ -1386,6 +1386,10 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
   p.sign = scale > 0.f ? 1 : scale < 0.f ? -1 : 0;
   p.idx = idx; p.page_table = page_table; p.cache = static_cast<const uint8_t*>(cache);
   p.q = static_cast<const uint16_t*>(q); p.o = static_cast<uint16_t*>(o); p.lse = lse;
+  p.rows = rows * heads;
+  CUtensorMap qmap;
+  e = tensor_map_2d(&qmap, q, HISA_BF16, static_cast<uint64_t>(p.rows), kAttnDqk, 32);
+  if (e != HISA_OK) return e;
   const size_t sel_smem = kv4_select_smem(top_k);
   e = cuda_check(cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(sel_smem)), "kv4_select attribute");
@@ -1401,7 +1405,7 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
     p.list = reinterpret_cast<int32_t*>(p.part_o + (plan.parts > 1 ? n * heads * plan.parts * kAttnDv : 0));
     p.count = p.list + n * plan.list_ld;
     p.part_lse = reinterpret_cast<float*>(p.count + n);
-    p.items = n * p.slices * p.parts;
+    p.items = static_cast<uint32_t>(n * p.slices * p.parts);        // < 2^31: pairs are, and parts only fill the SMs
     kv4_select_kernel<<<static_cast<unsigned>(n), kKv4SelThreads, sel_smem, st>>>(p);
     e = launch_check("kv4_select_kernel");
     if (e != HISA_OK) return e;
@@ -1419,7 +1423,7 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_attn_kernel, p), "launch kv4_attn_kernel");
+    e = cuda_check(cudaLaunchKernelEx(&cfg, kv4_attn_kernel, p, qmap), "launch kv4_attn_kernel");
     if (e != HISA_OK) return e;
     if (plan.parts > 1) {
       cfg.gridDim = dim3(static_cast<unsigned>(n * heads));
