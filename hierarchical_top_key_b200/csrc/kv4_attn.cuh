@@ -397,9 +397,8 @@ struct Kv4Walk {
   uint32_t at, step;
   int count;
   __device__ __forceinline__ explicit Kv4Walk(const Kv4AttnParams& params)
-      : p(params), at(sm100::cluster_id_x()), step(gridDim.x / 2) {
-    fetch();
-  }
+      : p(params), at(sm100::cluster_id_x()), step(gridDim.x / 2), count(0) {}
+  // To begin with, behind the selection, and by next().
   __device__ __forceinline__ void fetch() {
     count = at < p.items ? static_cast<int>(ld32_here(p.count + at / static_cast<uint32_t>(p.slices * p.parts))) : 0;
   }
@@ -525,16 +524,10 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(&sm->tmem_base, 512);
-  if (tid >= kKv4CorrBase && lane == 0) {              // the first query towards L2
-    const int rest = static_cast<int>(cluster_id_x()) / p.parts, h = rest % p.slices * kAttnHeads + (warp & 3) * 32;
-    if (h < p.heads)
-      prefetch_l2_bulk(p.q + ((p.row0 + rest / p.slices) * p.heads + h) * kAttnDqk, min(32, p.heads - h) * kAttnDqk * 2);
-  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();                                      // the peer's barriers exist before any remote arrive
   let_next_kernel_start();
-  wait_for_previous_kernel();                          // the lists
   tc_fence_after();
   const uint32_t tmem = sm->tmem_base;
   auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {    // by all lanes, the outcome warp-uniform
@@ -545,6 +538,10 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
   };
   Kv4Walk walk(p);
   Kv4Item it;
+  if (warp < kKv4CorrBase / 32) {                      // the lists; the output warps have a query to load first
+    wait_for_previous_kernel();
+    walk.fetch();
+  }
   auto warp_arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -859,23 +856,26 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     const float kInf = __int_as_float(0x7f800000);
     const uint32_t peer_fin_free = peer_addr(&sm->fin_free, peer);
     if (h == 0) mbar_arrive_expect_tx(&sm->fin_peer, kFinBytes);      // the first of the peer's sums
-    uint32_t live = 0, commands = 0, loaded = 0;       // queries put out, commands, queries loaded
+    uint32_t live = 0, commands = 0, loaded = 0;       // queries put out, commands, queries handed over
+    uint32_t fills = 0;                                // query loads
     bool ok = true;
 
     // The next query this CTA has tiles of its own for: one walk ahead.  Its
     // rows move towards L2 when it becomes the next.
-    if (lane == 0) tma_prefetch_desc(&qmap);
     Kv4Walk ahead(p);
     Kv4Item next;
     bool waiting = false;
     int q_row = 0;                                     // of the warp's 32 rows; past the end, zeros, for heads past the last
+    auto set_query = [&](int64_t item_row, int slice, bool prefetch) {
+      const int h0 = slice * kAttnHeads + quarter * 32;
+      const int64_t row = (p.row0 + item_row) * p.heads + h0;
+      q_row = static_cast<int>(h0 < p.heads ? row : p.rows);
+      if (prefetch && lane == 0 && h0 < p.heads)
+        prefetch_l2_bulk(p.q + row * kAttnDqk, min(32, p.heads - h0) * kAttnDqk * 2);
+    };
     auto find_query = [&]() {
       while ((waiting = ahead.next(next)) && next.own(rank) == 0) {}
-      if (!waiting) return;
-      const int h0 = next.slice * kAttnHeads + quarter * 32;
-      const int64_t row = (p.row0 + next.row) * p.heads + h0;
-      q_row = static_cast<int>(h0 < p.heads ? row : p.rows);
-      if (lane == 0 && h0 < p.heads) prefetch_l2_bulk(p.q + row * kAttnDqk, min(32, p.heads - h0) * kAttnDqk * 2);
+      if (waiting) set_query(next.row, next.slice, true);
     };
     // Panel pn of the warp's 32 rows into shared memory; no other warp reads or
     // writes them.  (Rows past the last head may be the next query's: their
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
     };
     auto panel_here = [&](int pn) {                    // after an abort too: the copy is not left in flight
       uint64_t* bar = &sm->q_in[quarter][pn % 3];
-      const uint32_t parity = (3 * loaded + pn / 3) & 1;
+      const uint32_t parity = (3 * fills + pn / 3) & 1;
       if (!mbar_wait(bar, parity, abort_flag)) mbar_drain(bar, parity);
       __syncwarp();
     };
@@ -916,11 +916,23 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
       tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
+      ++fills;
+    };
+    auto hand_over = [&]() {
       warp_arrive(&sm->q_full);
       ++loaded;
       find_query();
     };
+    // The first item's query does not depend on the selection: it is loaded
+    // while that runs, and used unless the item turns out to have no tile here.
+    const uint32_t first_item = walk.at, first_rest = first_item / static_cast<uint32_t>(p.parts);
+    set_query(first_rest / static_cast<uint32_t>(p.slices), static_cast<int>(first_rest % static_cast<uint32_t>(p.slices)), false);
+    load_query();
+    wait_for_previous_kernel();
+    walk.fetch();
+    ahead.fetch();
     find_query();
+    if (waiting && ahead.at == first_item + ahead.step) hand_over();
     auto timed_out = [&](uint64_t t0) -> bool {        // or the CTA is aborting, warp-uniform
       bool out = *abort_flag != 0;
       if (!out && globaltimer() - t0 > kWaitLimitNs) {
@@ -964,6 +976,7 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
           if (!ok) break;
           if (!command_here) {
             load_query();
+            hand_over();
             t0 = globaltimer();
             continue;
           }

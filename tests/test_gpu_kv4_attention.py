@@ -136,6 +136,37 @@ def test_padding_repeats_and_empty_rows(lib):
         c.check(q, idx, *c.run(q, idx), f"H={H}")
 
 
+@pytest.mark.parametrize("H", [16, 200])
+def test_many_queries_of_unlike_lengths(lib, H):
+    """More queries than pairs of SMs, so every pair takes several: the first of them empty, of one tile (none for
+    the pair's second CTA) or of one key, the later ones long, and the other way round at the end."""
+    Q, L, K = 400, 2000, 300
+    c = Case(1, L, 64, H + 3)
+    q = _q(1, Q, H, H + 3)
+    length = np.array([0, 1, 64, 65, 128, 129, 300, 40])
+    n = np.where(np.arange(Q) < 160, length[np.arange(Q) % 4], length[(np.arange(Q) * 5 // 3) % 8])
+    idx = synthetic.random_index_rows(1, Q, L, K, np.full((1, Q), L), seed=H)
+    idx[0, np.arange(K)[None, :] >= n[:, None]] = -1
+    o, lse = c.run(q, idx)
+    c.check(q, idx, o, lse, f"H={H}", rows=[(0, t) for t in range(0, Q, 7)])
+    assert np.array_equal(np.isneginf(lse.cpu().numpy()[0, :, 0]), n == 0)
+
+
+def test_a_query_does_not_see_its_neighbours(lib):
+    """Few heads: what stands behind a query's rows is the next query's, infinities and NaN among them."""
+    c = Case(1, 500, 64, 9)
+    q = _q(1, 3, 5, 9)
+    idx = synthetic.random_index_rows(1, 3, 500, 130, np.full((1, 3), 500), seed=9)
+    want, want_lse = c.run(q, idx)
+    c.check(q, idx, want, want_lse)
+    q[0, 1] = float("nan")
+    q[0, 1, 2] = float("inf")
+    q[0, 1, 4] = 1e30
+    o, lse = c.run(q, idx)
+    for t in (0, 2):
+        assert torch.equal(o[0, t], want[0, t]) and torch.equal(lse[0, t], want_lse[0, t])
+
+
 def test_split_and_whole_agree(lib):
     """The same rows alone (split over the keys) and within a batch that is not split."""
     L, K = 4000, 2048
