@@ -25,8 +25,8 @@
 //    run of its tiles and writes an fp32 output with its own lse;
 //    kv4_join_kernel joins the parts.
 //
-// Measured (128 heads, 2048 keys of 64K, 1024 queries): 0.69 ms = 851 TFLOP/s,
-// half the measured bf16 burst rate; the bf16 kernel of sparse_attn.cuh takes
+// Measured (128 heads, 2048 keys of 64K, 1024 queries): 0.67 ms = 868 TFLOP/s,
+// 0.52 of the measured bf16 burst rate; the bf16 kernel of sparse_attn.cuh takes
 // 1.02 ms.  Other divisions of the work, as whole kernels: features split and
 // fp32 partial logits exchanged (32 KB a tile each way) 1.08 ms; the logits
 // computed by both CTAs, nothing exchanged, 0.97 ms (shared memory's data path
@@ -107,11 +107,14 @@ __host__ __device__ inline uint32_t kv4_table_slots(int top_k) { return 4u * sta
 inline size_t kv4_select_smem(int top_k) { return (kv4_table_slots(top_k) + (top_k + 3) / 4 * 4) * 4; }
 
 // One block per query: the records of its selected positions, in the order of
-// the index row.  A hash table of places maps each position to the first place
-// of the row that holds it (the result does not depend on the order of the
-// atomics); a place is kept when it is that one.  A position whose page is
-// outside the cache is dropped and reported.  Thread t has places t, t + 512,
-// ...: all its loads are in flight together.
+// the index row.  Where the keys' bits fit into the table's memory, a bit a key
+// tells whether any position repeats; mostly none does and every place is kept.
+// Otherwise a hash table of places maps each position to the first place of the
+// row that holds it (the result does not depend on the order of the atomics); a
+// place is kept when it is that one: 64 rows of 2048 take 6.5 us by bits, 12 by
+// the table.  A position whose page is outside the
+// cache is dropped and reported.  Thread t has places t, t + 512, ...: all its
+// loads are in flight together.
 __global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4AttnParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(16) int count[kKv4Per * kKv4SelWarps], place[kKv4Per * kKv4SelWarps];
@@ -131,8 +134,13 @@ __global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4Att
     const int x = at < K ? __ldg(irow + at) : -1;
     v[u] = x < p.L ? x : -1;                            // negative: not a key
   }
-  for (uint32_t i = tid; i < slots / 4; i += kKv4SelThreads)
-    reinterpret_cast<uint4*>(table)[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  const bool bits = static_cast<uint32_t>(p.L) <= 32u * slots;
+  auto clear = [&](uint32_t words, uint32_t with) {    // to whole vectors: slots is a multiple of 4
+    for (uint32_t i = tid; i < (words + 3) / 4; i += kKv4SelThreads)
+      reinterpret_cast<uint4*>(table)[i] = make_uint4(with, with, with, with);
+  };
+  if (bits) clear((static_cast<uint32_t>(p.L) + 31) / 32, 0u);
+  else clear(slots, ~0u);
 #pragma unroll
   for (int u = 0; u < kKv4Per; ++u) {
     const int at = u * kKv4SelThreads + tid;
@@ -147,6 +155,18 @@ __global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4Att
     }
   }
   __syncthreads();
+  bool unique = false;
+  if (bits) {
+    uint32_t again = 0;
+#pragma unroll
+    for (int u = 0; u < kKv4Per; ++u)
+      if (v[u] >= 0) again |= atomicOr(&table[v[u] >> 5], 1u << (v[u] & 31)) >> (v[u] & 31) & 1u;
+    unique = __syncthreads_or(again) == 0;
+    if (!unique) {
+      clear(slots, ~0u);
+      __syncthreads();
+    }
+  }
   // every round tries all open places of the thread at once; a place that
   // finds another position in its slot goes to the next.  It ends: there are
   // more slots than places.
@@ -155,7 +175,7 @@ __global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4Att
 #pragma unroll
   for (int u = 0; u < kKv4Per; ++u) {
     at[u] = -1;
-    if (v[u] >= 0) {
+    if (v[u] >= 0 && !unique) {
       open |= 1u << u;
       at[u] = static_cast<int>(__umulhi(static_cast<uint32_t>(v[u]) * 0x9E3779B1u, slots));
     }
@@ -182,7 +202,7 @@ __global__ void __launch_bounds__(kKv4SelThreads) kv4_select_kernel(const Kv4Att
   uint32_t keep = 0;
 #pragma unroll
   for (int u = 0; u < kKv4Per; ++u) {
-    bool k = at[u] >= 0 && table[at[u]] == static_cast<uint32_t>(u * kKv4SelThreads + tid);
+    bool k = unique ? v[u] >= 0 : at[u] >= 0 && table[at[u]] == static_cast<uint32_t>(u * kKv4SelThreads + tid);
     if (k && rec[u] < 0) {
       record_status(HISA_ERR_INVALID_ARG);
       k = false;
