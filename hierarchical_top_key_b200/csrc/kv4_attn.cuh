@@ -33,8 +33,8 @@
 // is then busy 98 % of the time).  What bounds it now is the life of a tile's
 // buffers: 227 KB hold two own tiles' value halves but one of the rest of a row
 // and one of the peer's, so a tile's chain (keys 2K cycles, logit MMAs 1.3K,
-// softmax 2.7K, output MMA 0.5K) overlaps the next one's only in part: 4.6K
-// cycles a pair of tiles, 2.4K of them MMA.  Tried without gain: 4 or 8 warps
+// softmax 2.7K, output MMA 0.5K) overlaps the next one's only in part: 4.0K
+// cycles a pair of tiles, 2.4K of them MMA; a change of query adds 12K.  Tried without gain: 4 or 8 warps
 // on the own tiles' halves, row loads 64 bytes a lane pair, the shifts of the
 // decoding as multiplications, the weights to the own memory first.
 //
