@@ -136,6 +136,20 @@ def test_padding_repeats_and_empty_rows(lib):
         c.check(q, idx, *c.run(q, idx), f"H={H}")
 
 
+@pytest.mark.parametrize("L", [14848, 14849])
+def test_repeats_are_found_by_bits_and_by_the_table(lib, L):
+    """100 places have a table of 464 words = 14848 bits: one key more and the keys' bits no longer fit.  Rows
+    without a repeat, with one (the last key, in the row's first and last place), and with nothing else."""
+    K = 100
+    c = Case(1, L, 64, 11)
+    q = _q(1, 4, 16, 11)
+    idx = synthetic.random_index_rows(1, 4, L, K, np.full((1, 4), L), seed=11)
+    idx[0, 1, 0] = idx[0, 1, K - 1] = L - 1
+    idx[0, 2, :] = L - 1
+    idx[0, 3, ::2] = 0
+    c.check(q, idx, *c.run(q, idx), f"L={L}")
+
+
 @pytest.mark.parametrize("H", [16, 200])
 def test_many_queries_of_unlike_lengths(lib, H):
     """More queries than pairs of SMs, so every pair takes several: the first of them empty, of one tile (none for
