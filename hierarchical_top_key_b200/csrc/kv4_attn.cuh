@@ -1108,8 +1108,10 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
 }
 
 // Joins the parts of one (query, head): o = sum_i exp(lse_i - lse) o_i.  A part
-// without keys has lse_i = -inf and no output to read.  Eight parts' loads are
-// in flight at a time.
+// without keys has lse_i = -inf, weight 0 and no output to read; a part whose
+// lse is NaN makes o and lse NaN, also where no other part has keys (fmaxf
+// leaves it out of the maximum, which is then -inf).  Eight parts' loads are in
+// flight at a time.
 constexpr int kKv4MaxParts = kKv4MaxK / kAttnTileN;
 __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
   __shared__ float weight[kKv4MaxParts];
@@ -1125,7 +1127,7 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnParams p) {
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
   float z = 0.f;
   for (int i = lane; i < p.parts; i += 32) {
-    const float w = top > -kInf ? expf(pl[i] - top) : 0.f;
+    const float w = pl[i] == -kInf ? 0.f : expf(pl[i] - top);
     z += w;
     if (threadIdx.x < 32) weight[i] = w;
   }

@@ -406,3 +406,54 @@ def test_a_decode_step_of_all_of_them(lib):
     o16, _ = hb.hisa_sparse_attention(qa, latent.view(B, L, 576), idx, scale=SCALE)
     rel = (o16.float() - o.float()).norm() / o16.float().norm()
     assert rel < 0.15
+
+
+def _not_finite(value, what):
+    assert value.isnan().all(), f"{what}: {value.flatten()[:4].tolist()}"
+
+
+@pytest.mark.parametrize("Q", [1, 90])
+@pytest.mark.parametrize("H", [16, 128])
+def test_a_query_head_that_is_not_finite(lib, H, Q):
+    """NaN, infinities and an overflow in chosen heads of a query make just those heads NaN, whether the query is
+    alone (split over its keys) or one of 90 (whole); the other heads keep their bits."""
+    L, K = 3000, 2048
+    c = Case(1, L, 64, H + 41)
+    q = _q(1, Q, H, H + 41)
+    idx = synthetic.random_index_rows(1, Q, L, K, np.full((1, Q), L), seed=H + 41)
+    want, want_lse = c.run(q, idx)
+    q[0, 0, 1, 7] = float("nan")
+    q[0, 0, 4, 560] = float("inf")                  # a positional feature: no key's is 0, about half are negative
+    q[0, 0, 9, 560] = float("-inf")
+    q[0, 0, 11] = 3e38                              # fp32 dot products of both infinities
+    o, lse = c.run(q, idx)
+    bad = [1, 4, 9, 11]
+    rest = [h for h in range(H) if h not in bad]
+    _not_finite(o[0, 0, bad], "o")
+    _not_finite(lse[0, 0, bad], "lse")
+    assert torch.equal(o[0, 0, rest], want[0, 0, rest]) and torch.equal(lse[0, 0, rest], want_lse[0, 0, rest])
+    assert torch.equal(o[0, 1:], want[0, 1:]) and torch.equal(lse[0, 1:], want_lse[0, 1:])
+
+
+@pytest.mark.parametrize("feature", [float("nan"), float("inf")])
+def test_keys_that_are_not_finite_in_every_part_with_keys(lib, feature):
+    """A split row all of whose parts with keys hold a key with a logit of NaN or +inf: one part of one tile, one key
+    alone, and every part.  NaN, as within a batch that is not split."""
+    L, K = 3000, 2048
+    c = Case(1, L, 64, 43)
+    q = _q(1, 90, 128, 43)
+    q[..., 512] = q[..., 512].abs() + 0.5
+    idx = synthetic.random_index_rows(1, 90, L, K, np.full((1, 90), L), seed=43)
+    idx[0, 0, 40:] = -1                             # one tile: only the first part has keys
+    idx[0, 1, 1:] = -1
+    for s in {int(idx[0, 0, 39]), int(idx[0, 1, 0])} | set(idx[0, 2, ::32].tolist()):
+        row = torch.from_numpy(c.kv[0, s:s + 1]).to(torch.bfloat16).cuda()
+        row[0, 512] = feature
+        _hb().hisa_kv4_write(row, c.slots[0, s].view(1).cuda(), c.cache)
+    o, lse = c.run(q, idx)
+    for t in range(3):
+        _not_finite(o[0, t], f"whole o, query {t}")
+        _not_finite(lse[0, t], f"whole lse, query {t}")
+        o1, l1 = c.run(q[:, t:t + 1], idx[:, t:t + 1].copy())
+        _not_finite(o1, f"split o, query {t}")
+        _not_finite(l1, f"split lse, query {t}")
