@@ -787,9 +787,10 @@ __global__ void __launch_bounds__(kKv4Threads, 1) kv4_attn_kernel(const Kv4AttnP
         }
         tc_fence_before();
         warp_arrive(&sm->s_empty);
-        if (p.sign != 1) {
+        if (p.sign != 1) {                             // a product: at a scale of 0 a NaN or infinity becomes NaN
+          const float sign = static_cast<float>(p.sign);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = p.sign == 0 ? 0.f : -s[i];
+          for (int i = 0; i < 32; ++i) s[i] *= sign;
         }
         const int nk = it.keys_of(2 * k + static_cast<int>(rank)) - 32 * g;
         if (nk < 32) {

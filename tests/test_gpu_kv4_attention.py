@@ -457,3 +457,20 @@ def test_keys_that_are_not_finite_in_every_part_with_keys(lib, feature):
         o1, l1 = c.run(q[:, t:t + 1], idx[:, t:t + 1].copy())
         _not_finite(o1, f"split o, query {t}")
         _not_finite(l1, f"split lse, query {t}")
+
+
+@pytest.mark.parametrize("Q", [1, 90])
+def test_a_scale_of_zero_keeps_what_is_not_finite(lib, Q):
+    """0 times a dot product that is NaN or infinite is NaN; every other head weighs all keys alike."""
+    c = Case(1, 600, 64, 47)
+    q = _q(1, Q, 128, 47)
+    idx = synthetic.random_index_rows(1, Q, 600, 300, np.full((1, Q), 600), seed=47)
+    want, want_lse = c.run(q, idx, scale=0.0)
+    c.check(q * 0, idx, want, want_lse, "scale 0", rows=[(0, 0)])
+    q[0, 0, 2, 100] = float("nan")
+    q[0, 0, 5, 570] = float("inf")
+    o, lse = c.run(q, idx, scale=0.0)
+    rest = [h for h in range(128) if h not in (2, 5)]
+    _not_finite(o[0, 0, [2, 5]], "o")
+    _not_finite(lse[0, 0, [2, 5]], "lse")
+    assert torch.equal(o[0, 0, rest], want[0, 0, rest]) and torch.equal(lse[0, 0, rest], want_lse[0, 0, rest])
