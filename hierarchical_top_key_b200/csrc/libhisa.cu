@@ -119,20 +119,38 @@ int num_sms() {
 // ------------------------------------------------------------ TMA descriptors
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
+PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
+
+// The driver's functions that descriptors need, and a context to call them in:
+// a host thread's first call may be one of these, and only the runtime's own
+// functions bind its device's context to it.
+hisa_status encode_ready() {
+  if (!g_encode_tiled || !g_ctx_current) {
+    void *encode = nullptr, *current = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &encode, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !encode)
+      return fail(HISA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    e = cudaGetDriverEntryPoint("cuCtxGetCurrent", &current, cudaEnableDefault, &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !current)
+      return fail(HISA_ERR_CUDA, "cuCtxGetCurrent entry point unavailable");
+    g_ctx_current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(current);
+    g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(encode);
+  }
+  CUcontext ctx = nullptr;
+  if (g_ctx_current(&ctx) == CUDA_SUCCESS && ctx) return HISA_OK;
+  int dev = 0;
+  hisa_status e = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  return e != HISA_OK ? e : cuda_check(cudaSetDevice(dev), "cudaSetDevice");
+}
 
 // A 2D map over [rows, cols] with boxes of box_rows x (128 bytes of columns,
 // or box_cols columns), 128-byte swizzle unless another is given.
 hisa_status tensor_map_2d(CUtensorMap* map, const void* base, int dtype, uint64_t rows, uint64_t cols,
                           uint32_t box_rows, uint64_t row_stride_elems = 0, uint32_t box_cols = 0,
                           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  if (!g_encode_tiled) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
-      return fail(HISA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
-    g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
+  hisa_status e = encode_ready();
+  if (e != HISA_OK) return e;
   const int es = elem_bytes(dtype);
   const CUtensorMapDataType ty = dtype == HISA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cuuint64_t dims[2] = {cols, rows};
@@ -152,11 +170,8 @@ hisa_status tensor_map_2d(CUtensorMap* map, const void* base, int dtype, uint64_
 // [panel][row][128 B] in shared memory.
 hisa_status tensor_map_3d_panels(CUtensorMap* map, const void* base, int dtype, uint64_t rows, uint64_t cols,
                                  uint32_t box_rows) {
-  if (!g_encode_tiled) {
-    CUtensorMap probe;
-    hisa_status e = tensor_map_2d(&probe, base, dtype, rows, cols, 1);   // resolves the entry point
-    if (e != HISA_OK) return e;
-  }
+  hisa_status e = encode_ready();
+  if (e != HISA_OK) return e;
   const int es = elem_bytes(dtype);
   const uint64_t panel = 128 / es;
   const CUtensorMapDataType ty = dtype == HISA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
