@@ -8,7 +8,9 @@
 #include <cstdarg>
 #include <algorithm>
 #include <cmath>
+#include <map>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include <cudaTypedefs.h>
@@ -46,6 +48,24 @@ hisa_status cuda_check(cudaError_t e, const char* what) {
 }
 
 hisa_status launch_check(const char* what) { return cuda_check(cudaGetLastError(), what); }
+
+// Lets `kern` be launched with `bytes` of dynamic shared memory on the current
+// device.  The limit is the kernel's, one for all host threads: it is only ever
+// raised, so that no call lowers it between another's request and its launch.
+template <typename K>
+hisa_status allow_smem(K* kern, size_t bytes, const char* what) {
+  static std::mutex mutex;
+  static std::map<std::pair<int, const void*>, size_t> allowed;
+  int dev = 0;
+  hisa_status e = cuda_check(cudaGetDevice(&dev), what);
+  if (e != HISA_OK) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  size_t& now = allowed[{dev, reinterpret_cast<const void*>(kern)}];
+  if (bytes <= now) return HISA_OK;
+  e = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)), what);
+  if (e == HISA_OK) now = bytes;
+  return e;
+}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
@@ -85,8 +105,7 @@ hisa_status launch_score_rows(const hisa_shape* s, const void* q, const float* q
   const int kpc = 2048;
   const size_t smem = SimtTile<DT, HT>::smem_bytes(s->head_dim);
   auto kern = score_rows_simt_kernel<DT, HT>;
-  hisa_status e = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(smem)), "score_rows attribute");
+  hisa_status e = allow_smem(kern, smem, "score_rows attribute");
   if (e != HISA_OK) return e;
   dim3 grid(static_cast<unsigned>(nrows), static_cast<unsigned>(ceil_div(L, kpc)));
   kern<<<grid, kSimtThreads, smem, st>>>(static_cast<const uint8_t*>(q), qsc, w,
@@ -245,8 +264,7 @@ hisa_status launch_dense_tc(const hisa_shape* s, const CUtensorMap& qmap, const 
   }
   const size_t smem = dense_smem_bytes(rb, p.stages, p.q_bufs);
   auto kern = dense_score_tc_kernel<DT, H>;
-  hisa_status e = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(smem)), "dense_score_tc attribute");
+  hisa_status e = allow_smem(kern, smem, "dense_score_tc attribute");
   if (e != HISA_OK) return e;
   const int64_t units = static_cast<int64_t>(p.ngroups) * p.max_chunks;
   const int grid = static_cast<int>(std::min<int64_t>(units, sms));
@@ -324,8 +342,7 @@ hisa_status launch_token_simt(const hisa_shape* s, const void* q, const float* q
   const size_t smem = SimtTile<DT, HT>::smem_bytes(s->head_dim) +
                       static_cast<size_t>(s->top_m) * s->block_size * sizeof(uint32_t);
   auto kern = token_stage_simt_kernel<DT, HT>;
-  hisa_status e = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(smem)), "token_stage attribute");
+  hisa_status e = allow_smem(kern, smem, "token_stage attribute");
   if (e != HISA_OK) return e;
   kern<<<static_cast<unsigned>(rows_of(s)), kSimtThreads, smem, st>>>(
       static_cast<const uint8_t*>(q), qsc, w, static_cast<const uint8_t*>(k), ksc, nvis, bidx,
@@ -433,8 +450,7 @@ hisa_status launch_token_tc(const hisa_shape* s, const void* q, const float* qsc
             : tensor_map_2d(&km, k, s->dtype, key_rows, s->head_dim, s->block_size);
   if (e != HISA_OK) return e;
   auto kern = token_tc_kernel<DT, H>;
-  e = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
-                 "token_tc attribute");
+  e = allow_smem(kern, smem, "token_tc attribute");
   if (e != HISA_OK) return e;
   const int grid = static_cast<int>(std::min<int64_t>(p.rows * parts, num_sms()));
   kern<<<grid, kTokThreads, smem, st>>>(qm, km, p);
@@ -514,8 +530,7 @@ hisa_status launch_flat_fallback(const hisa_shape* s, const void* q, const float
                                  const int32_t* fail_rows, float* scratch, int fb_ctas, int32_t* oi, float* os,
                                  cudaStream_t st) {
   auto run = [&](auto kern, size_t smem) {
-    hisa_status e = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    static_cast<int>(smem)), "flat_fallback attribute");
+    hisa_status e = allow_smem(kern, smem, "flat_fallback attribute");
     if (e != HISA_OK) return e;
     kern<<<fb_ctas, kSimtThreads, smem, st>>>(static_cast<const uint8_t*>(q), qsc, w, static_cast<const uint8_t*>(k),
                                               ksc, nvis, row0, s->num_queries, s->heads, s->head_dim, s->num_keys,
@@ -602,8 +617,7 @@ hisa_status sort_scored_rows(int32_t* idx, float* score, int64_t rows, int k, cu
   if (!score || rows == 0) return HISA_OK;
   const int n = sort_pow2(k);
   const int smem = n * static_cast<int>(sizeof(uint64_t));
-  hisa_status e = cuda_check(cudaFuncSetAttribute(sort_scored_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  smem), "sort_scored_rows attribute");
+  hisa_status e = allow_smem(sort_scored_rows_kernel, smem, "sort_scored_rows attribute");
   if (e != HISA_OK) return e;
   const int per_sm = std::max(1, std::min(8, static_cast<int>(kSmemBudgetRows / std::max(smem, 1))));
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * per_sm));
@@ -1045,8 +1059,7 @@ hisa_status dsa_flat_indexer_topk(const void* q, const float* q_scale, const flo
   for (const RowChunk& c : chunks) max_rows = std::max(max_rows, c.nrows);
   uint32_t* minmax = reinterpret_cast<uint32_t*>(ws + max_rows * ld);
   const bool fused_range = dense_tc_ok(s);
-  e = cuda_check(cudaFuncSetAttribute(flat_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(sizeof(TwoPassSmem))), "flat_select attribute");
+  e = allow_smem(flat_select_kernel, sizeof(TwoPassSmem), "flat_select attribute");
   if (e != HISA_OK) return e;
   for (const RowChunk& c : chunks) {
     if (fused_range) {
@@ -1126,8 +1139,7 @@ hisa_status hisa_sparse_attention(const void* q, const void* kv, const int32_t* 
                     CU_TENSOR_MAP_SWIZZLE_64B);
   if (e != HISA_OK) return e;
   const size_t smem = attn_smem_bytes();
-  e = cuda_check(cudaFuncSetAttribute(sparse_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem)), "sparse_attn attribute");
+  e = allow_smem(sparse_attn_kernel, smem, "sparse_attn attribute");
   if (e != HISA_OK) return e;
   AttnParams p{};
   p.rows = rows; p.Q = num_queries; p.L = num_keys; p.slices = slices; p.top_k = top_k;
@@ -1406,11 +1418,9 @@ hisa_status hisa_sparse_attention_kv4(const void* q, const void* cache, int32_t 
   e = tensor_map_2d(&qmap, q, HISA_BF16, static_cast<uint64_t>(p.rows), kAttnDqk, 32);
   if (e != HISA_OK) return e;
   const size_t sel_smem = kv4_select_smem(top_k);
-  e = cuda_check(cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(sel_smem)), "kv4_select attribute");
+  e = allow_smem(kv4_select_kernel, sel_smem, "kv4_select attribute");
   if (e != HISA_OK) return e;
-  e = cuda_check(cudaFuncSetAttribute(kv4_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(kKv4SmemBytes)), "kv4_attn attribute");
+  e = allow_smem(kv4_attn_kernel, kKv4SmemBytes, "kv4_attn attribute");
   if (e != HISA_OK) return e;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   for (p.row0 = 0; p.row0 < rows; p.row0 += chunk) {

@@ -474,3 +474,44 @@ def test_a_scale_of_zero_keeps_what_is_not_finite(lib, Q):
     _not_finite(o[0, 0, [2, 5]], "o")
     _not_finite(lse[0, 0, [2, 5]], "lse")
     assert torch.equal(o[0, 0, rest], want[0, 0, rest]) and torch.equal(lse[0, 0, rest], want_lse[0, 0, rest])
+
+
+def test_two_threads_with_index_rows_of_unlike_lengths(lib):
+    """Each thread on its stream, one with the longest index rows, one with short ones: every call is accepted."""
+    import threading
+    hb = _hb()
+    L, calls = 5000, 3000
+    c = Case(1, L, 64, 53)
+    table = c.table.cuda()
+    jobs = []
+    for K in (4096, 64):
+        q = _q(1, 1, 128, K)
+        idx = synthetic.random_index_rows(1, 1, L, K, np.full((1, 1), L), seed=K)
+        jobs.append(dict(K=K, q=q, idx=idx, dq=q.cuda(), di=torch.from_numpy(idx).cuda(), stream=torch.cuda.Stream(),
+                         o=torch.empty((1, 1, 128, 512), dtype=torch.bfloat16, device="cuda"),
+                         lse=torch.empty((1, 1, 128), device="cuda"), bad=[],
+                         ws=torch.empty(hb.workspace_size(hb.OP_ATTENTION_KV4,
+                                                          hb.Shape(1, L, 1, 128, 0, 0, 0, K, hb.HISA_BF16)),
+                                        dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def work(j):
+        start.wait()
+        for _ in range(calls):
+            status = lib.hisa_sparse_attention_kv4(
+                j["dq"].data_ptr(), c.cache.data_ptr(), c.cache.shape[0], c.page, table.data_ptr(), j["di"].data_ptr(),
+                1, 1, L, 128, j["K"], SCALE, j["o"].data_ptr(), j["lse"].data_ptr(), j["ws"].data_ptr(),
+                j["ws"].numel(), j["stream"].cuda_stream)
+            if status:
+                j["bad"].append(status)
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    hb.get_status()
+    for j in jobs:
+        assert not j["bad"], f"top_k={j['K']}: {len(j['bad'])} of {calls} calls refused, status {j['bad'][0]}"
+        c.check(j["q"], j["idx"], j["o"], j["lse"], f"K={j['K']}")

@@ -1,4 +1,5 @@
 """The library called from several host threads."""
+import ctypes
 import threading
 
 import pytest
@@ -50,3 +51,44 @@ def test_a_threads_first_call(lib):
     got = _in_a_new_thread(lambda: hb.hisa_sparse_attention_kv4(q, cache, table, idx, scale=0.07, num_keys=L))
     torch.cuda.synchronize()
     assert torch.equal(got[0], want4[0]) and torch.equal(got[1], want4[1])
+
+
+def test_scored_rows_of_unlike_lengths(lib):
+    """Two threads at once, each on its stream: the flat indexer with scores, rows of 16384 sorted in 128 KB of shared
+    memory, rows of 16 in 128 bytes.  The limit is the kernel's, one for all threads."""
+    from hierarchical_top_key_b200 import binding as hb
+    L, calls = 20000, 1500
+    g = torch.Generator().manual_seed(0)
+    q = torch.randn((1, 1, 16, 64), generator=g).to(torch.bfloat16).cuda()
+    k = torch.randn((1, L, 64), generator=g).to(torch.bfloat16).cuda()
+    w = torch.rand((1, 1, 16), generator=g).cuda()
+    nv = torch.full((1, 1), L, dtype=torch.int32, device="cuda")
+    want = {K: hb.dsa_flat_indexer_topk(q, w, k, nv, top_k=K, want_scores=True) for K in (16384, 16)}
+    jobs = []
+    for K in want:
+        s = hb.make_shape(q, k, 1, 1, K)
+        jobs.append(dict(K=K, s=s, stream=torch.cuda.Stream(), bad=[],
+                         idx=torch.empty((1, 1, K), dtype=torch.int32, device="cuda"),
+                         sc=torch.empty((1, 1, K), device="cuda"),
+                         ws=torch.empty(max(16, hb.workspace_size(hb.OP_FLAT, s)), dtype=torch.uint8, device="cuda")))
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def work(j):
+        start.wait()
+        for _ in range(calls):
+            status = lib.dsa_flat_indexer_topk(q.data_ptr(), None, w.data_ptr(), k.data_ptr(), None, nv.data_ptr(),
+                                               ctypes.byref(j["s"]), j["idx"].data_ptr(), j["sc"].data_ptr(),
+                                               j["ws"].data_ptr(), j["ws"].numel(), j["stream"].cuda_stream)
+            if status:
+                j["bad"].append((status, lib.hisa_last_error()))
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    hb.get_status()
+    for j in jobs:
+        assert not j["bad"], f"top_k={j['K']}: {len(j['bad'])} of {calls} calls refused: {j['bad'][0]}"
+        assert torch.equal(j["idx"], want[j["K"]][0]) and torch.equal(j["sc"], want[j["K"]][1])
