@@ -54,6 +54,13 @@ __device__ __forceinline__ float2 turn_of(int32_t pos, uint64_t turns, float amp
   return make_float2(c * amplitude, s * amplitude * sign);
 }
 
+// The pair (a, b) turned by t = (cos, sin).  The product with the sine is rounded
+// before the sum in every kernel: a rotation in place may spread the same rows
+// over the lanes in another way than one out of place, and gives the same bits.
+// (A norm's sums follow the lanes: where they differ, so may its last bits.)
+__device__ __forceinline__ float turn_first(float a, float b, float2 t) { return __fmaf_rn(a, t.x, -__fmul_rn(b, t.y)); }
+__device__ __forceinline__ float turn_second(float a, float b, float2 t) { return __fmaf_rn(b, t.x, __fmul_rn(a, t.y)); }
+
 template <int DT> __device__ __forceinline__ float load_elem(const void* p, int64_t i);
 template <> __device__ __forceinline__ float load_elem<DT_F32>(const void* p, int64_t i) {
   return static_cast<const float*>(p)[i];
@@ -112,8 +119,8 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) norm_rotary_rows_kernel(con
     const float2 t = turn_of(pos, turns64(p.inv_freq[i]), p.amplitude, p.sign);
     const int ja = p.offset + (p.interleaved ? 2 * i : i), jb = p.interleaved ? ja + 1 : ja + half;
     const float va = b[ja], vb = b[jb];
-    b[ja] = va * t.x - vb * t.y;
-    b[jb] = vb * t.x + va * t.y;
+    b[ja] = turn_first(va, vb, t);
+    b[jb] = turn_second(va, vb, t);
   }
   __syncwarp();
   for (int j = p.first + lane; j < p.last; j += 32) store_elem<DT>(p.out, oi + j, b[j]);
@@ -299,8 +306,8 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
           for (int e = 0; e < E; ++e) {
             const float2 t = turn[jr + e];
             const float c = x[e], d = m[e];
-            x[e] = c * t.x - d * t.y;
-            m[e] = d * t.x + c * t.y;
+            x[e] = turn_first(c, d, t);
+            m[e] = turn_second(c, d, t);
           }
         }
         *reinterpret_cast<uint4*>(outr + j * ES) = pack_vec<DT>(x);
@@ -319,8 +326,8 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
             for (int e = 0; e < E; e += 2) {
               const float2 t = turn[(jr + e) >> 1];
               const float c = x[e], d = x[e + 1];
-              x[e] = c * t.x - d * t.y;
-              x[e + 1] = d * t.x + c * t.y;
+              x[e] = turn_first(c, d, t);
+              x[e + 1] = turn_second(c, d, t);
             }
           } else {
             float m[E];
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
             normed(m, mate[PAIRS == PAIRS_RELOAD ? v : 0], low ? j + half : j - half, v, false);
             const float2* tv = turn + (low ? jr : jr - half);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = x[e] * tv[e].x + m[e] * (low ? -tv[e].y : tv[e].y);
+            for (int e = 0; e < E; ++e) x[e] = low ? turn_first(x[e], m[e], tv[e]) : turn_second(m[e], x[e], tv[e]);
           }
         }
         *reinterpret_cast<uint4*>(outr + j * ES) = pack_vec<DT>(x);

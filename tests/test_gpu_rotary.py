@@ -210,3 +210,60 @@ def test_values_that_are_not_finite_stay_in_their_row(lib):
     touched[2, 1] = touched[4, 0] = True
     assert torch.equal(got[~touched.cuda()], want[~touched.cuda()])
     assert got[2, 1].isnan().all()
+
+
+def _check_norm_rotary(x, pos, f, norm, norm_dim, w, b, offset, inter, out, what=""):
+    """out against the oracle, within the bounds at the top."""
+    xn, pn, fn = x.double().cpu().numpy(), pos.cpu().numpy(), f.cpu().numpy()
+    wn, bn = w.cpu().numpy(), None if b is None else b.cpu().numpy()
+    d, rot = xn.shape[-1], 2 * len(fn)
+    y = orot.norm(xn, norm, norm_dim, wn, bn, float(np.float32(1e-5)))
+    part = xn[..., :norm_dim]
+    mean = part.mean(-1, keepdims=True) if norm == "layer" else 0.0
+    rms = np.sqrt(((part - mean) ** 2).mean(-1, keepdims=True) + 1e-5)
+    e = np.zeros(xn.shape)
+    e[..., :norm_dim] = 64 * U * (np.abs(part) + np.abs(part).mean(-1, keepdims=True)) / rms * np.abs(wn) + \
+        (2 * U * np.abs(bn) if bn is not None else 0)
+    inside = np.zeros(d, bool)
+    inside[offset:offset + rot] = True
+    e = np.where(inside, _pair_size(e, fn, offset, inter, 1.0), e) + \
+        16 * U * _pair_size(np.asarray(y, np.float64), fn, offset, inter, 1.0)
+    _compare(out, orot.rotate(y, pn, fn, offset, inter), e, x.dtype, what)
+
+
+@pytest.mark.parametrize("T,H,d,rot,offset,dtype,norm,inter", [
+    (20011, 1, 576, 64, 512, torch.bfloat16, "rms", True), (20011, 1, 576, 64, 512, torch.bfloat16, "rms", False),
+    (40009, 1, 128, 64, 0, torch.bfloat16, "layer", True), (4099, 40, 128, 128, 0, torch.float32, "rms", False),
+    (4099, 40, 128, 128, 0, torch.float32, "layer", True), (5003, 64, 128, 64, 0, torch.bfloat16, None, True),
+    (5003, 64, 128, 64, 0, torch.bfloat16, None, False), (1009, 64, 576, 64, 512, torch.bfloat16, None, False),
+    (3001, 40, 80, 64, 16, torch.float32, None, False)])
+def test_more_rows_than_a_wave_of_blocks(lib, T, H, d, rot, offset, dtype, norm, inter):
+    """Blocks that take several rows a lane group, ragged at the end: every row as in calls of few tokens, whose
+    blocks take one, out of place and in place (strided); some against the oracle."""
+    hb = _hb()
+    x, pos = _inputs(T, H, d, dtype, seed=T + d, gap=64, last=160000)
+    f, amp = hb.rotary_inv_freq(rot, scaling="ramp", factor=8.0) if norm is None else hb.rotary_inv_freq(rot)
+    nd = 512 if d == 576 else d
+    g = torch.Generator().manual_seed(T)
+    w = (1 + 0.3 * torch.randn(nd, generator=g)).cuda()
+    b = torch.randn(nd, generator=g).cuda() if norm == "layer" else None
+
+    def run(x, pos, out=None):
+        if norm is None:
+            return hb.hisa_rotary(x, pos, f, offset=offset, interleaved=inter, amplitude=amp, out=out)
+        return hb.hisa_norm_rotary(x, pos, f, weight=w, bias=b, norm=norm, eps=1e-5, norm_dim=nd, offset=offset,
+                                   interleaved=inter, out=out)
+    got = run(x, pos)
+    few = max(1, 800 // H)
+    for t in range(0, T, few):
+        assert torch.equal(got[t:t + few], run(x[t:t + few], pos[t:t + few])), f"tokens {t} to {t + few}"
+    at = torch.unique(torch.cat([torch.tensor([0, 1, T - 2, T - 1]), torch.randint(0, T, (20,), generator=g)]))
+    xa, pa, ga = x[at.cuda()], pos[at.cuda()], got[at.cuda()]
+    if norm is None:
+        xn, fn = xa.double().cpu().numpy(), f.cpu().numpy()
+        _compare(ga, orot.rotate(xn, pa.cpu().numpy(), fn, offset, inter, amp),
+                 16 * U * _pair_size(xn, fn, offset, inter, amp), dtype)
+    else:
+        _check_norm_rotary(xa, pa, f, norm, nd, w, b, offset, inter, ga)
+    assert run(x, pos, out=x) is x
+    assert torch.equal(x, got)
