@@ -267,3 +267,23 @@ def test_more_rows_than_a_wave_of_blocks(lib, T, H, d, rot, offset, dtype, norm,
         _check_norm_rotary(xa, pa, f, norm, nd, w, b, offset, inter, ga)
     assert run(x, pos, out=x) is x
     assert torch.equal(x, got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True], ids=["half", "interleaved"])
+@pytest.mark.parametrize("norm,biased", [("rms", False), ("layer", True), ("layer", False)])
+@pytest.mark.parametrize("T,H,d,rot,offset,norm_dim", [
+    (33, 4, 128, 128, 0, 128), (37, 3, 128, 64, 0, 128), (9, 2, 128, 64, 64, 128),    # half-layout partners in a lane
+    (21, 5, 80, 64, 16, 80), (12, 2, 192, 64, 128, 192), (7, 1, 576, 64, 512, 576), (3, 2, 1024, 1024, 0, 1024),
+    (11, 3, 96, 64, 16, 48), (14, 4, 128, 64, 0, 32)])                                # the norm ends inside the part
+def test_norms_of_whole_vectors(lib, T, H, d, rot, offset, norm_dim, norm, biased, inter, dtype):
+    """Rows, parts and norms of whole 16-byte vectors, both layouts, weight and bias unlike 1 and 0."""
+    hb = _hb()
+    x, pos = _inputs(T, H, d, dtype, seed=d + rot + norm_dim)
+    f, _ = hb.rotary_inv_freq(rot)
+    g = torch.Generator().manual_seed(norm_dim)
+    w = (1 + 0.3 * torch.randn(norm_dim, generator=g)).cuda()
+    b = torch.randn(norm_dim, generator=g).cuda() if biased else None
+    out = hb.hisa_norm_rotary(x, pos, f, weight=w, bias=b, norm=norm, eps=1e-5, norm_dim=norm_dim, offset=offset,
+                              interleaved=inter)
+    _check_norm_rotary(x, pos, f, norm, norm_dim, w, b, offset, inter, out)
