@@ -495,7 +495,17 @@ def _on(device: int, name: str, *tensors):
             raise ValueError(f"all tensors of {name} must be on one device (cuda:{device}), got one on {t.device}")
 
 
+def _no_gradient(name: str, *tensors):
+    """Refuses tensors that want a gradient through `name`, which computes none."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} computes no gradient and got a tensor that requires one: call it under "
+                                 "torch.no_grad() or with detached tensors")
+
+
 def _rotary(name, x, positions, inv_freq, offset, out, weight=None, bias=None):
+    _no_gradient(name, x, inv_freq, out, weight, bias)
     tokens, heads, dim, ts, hs = _rows_of(x, "x")
     if x.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
@@ -523,7 +533,9 @@ def hisa_rotary(x, positions, inv_freq, *, offset: int = 0, interleaved: bool = 
     and head strides) turned by positions (int32, x's leading shape).  inv_freq
     (float64) and amplitude come from rotary_inv_freq.  out=x turns in place
     and touches only the turned features; reverse=True turns back (the
-    gradient).  Returns out."""
+    gradient, for a backward pass of the caller's own: nothing is recorded, and
+    tensors that require a gradient are refused outside torch.no_grad()).
+    Returns out."""
     tokens, heads, dim, ts, hs, out, ots, ohs = _rotary("hisa_rotary", x, positions, inv_freq, offset, out)
     with _device_of(x):
         _check(load().hisa_rotary(x.data_ptr(), ts, hs, positions.data_ptr(), inv_freq.data_ptr(), tokens, heads, dim,
@@ -537,7 +549,8 @@ def hisa_norm_rotary(x, positions, inv_freq, *, weight, bias=None, norm: str = "
                      amplitude: float = 1.0, out: Optional[torch.Tensor] = None):
     """The RMS ("rms") or layer ("layer") norm of each head's features [0, norm_dim)
     (default: all) with fp32 weight (and bias), then hisa_rotary's turn, in
-    one pass.  Returns out (out=x works in place)."""
+    one pass.  Returns out (out=x works in place).  Tensors that require a gradient
+    are refused outside torch.no_grad()."""
     tokens, heads, dim, ts, hs, out, ots, ohs = _rotary("hisa_norm_rotary", x, positions, inv_freq, offset, out, weight,
                                                         bias)
     if norm not in NORMS:

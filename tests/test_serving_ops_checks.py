@@ -182,3 +182,19 @@ def test_cache_oracle():
     back = lc.decode(rec)
     assert np.array_equal(back[:512], row)
     assert np.array_equal((back[512:].astype(np.float32).view(np.uint32) >> 16), np.arange(64))
+
+
+def test_rotary_refuses_what_wants_a_gradient():
+    """They compute no gradient: a tensor that wants one is refused while gradients are recorded, before all else."""
+    x = torch.zeros((4, 2, 128), dtype=torch.bfloat16)
+    pos, f, w = torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.float64), torch.ones(128)
+    for call, names in ((lambda a: hb.hisa_rotary(a["x"], pos, a["f"], out=a["out"]), ("x", "f", "out")),
+                        (lambda a: hb.hisa_norm_rotary(a["x"], pos, a["f"], weight=a["w"], bias=a["b"], norm="layer",
+                                                       out=a["out"]), ("x", "f", "out", "w", "b"))):
+        for name in names:
+            a = dict(x=x, f=f, w=w, b=w, out=x.clone())
+            a[name] = a[name].clone().requires_grad_()
+            with pytest.raises(ValueError, match="gradient"):
+                call(a)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # the next check
+                call(a)
