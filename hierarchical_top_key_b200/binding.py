@@ -551,6 +551,8 @@ def hisa_norm_rotary(x, positions, inv_freq, *, weight, bias=None, norm: str = "
     (default: all) with fp32 weight (and bias), then hisa_rotary's turn, in
     one pass.  Returns out (out=x works in place).  Tensors that require a gradient
     are refused outside torch.no_grad()."""
+    if weight is None:
+        raise ValueError("weight must be given (ones for a norm without one)")
     tokens, heads, dim, ts, hs, out, ots, ohs = _rotary("hisa_norm_rotary", x, positions, inv_freq, offset, out, weight,
                                                         bias)
     if norm not in NORMS:

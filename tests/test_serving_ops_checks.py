@@ -198,3 +198,9 @@ def test_rotary_refuses_what_wants_a_gradient():
                 call(a)
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # the next check
                 call(a)
+
+
+def test_norm_rotary_refuses_a_missing_weight():
+    with pytest.raises(ValueError, match="weight"):
+        hb.hisa_norm_rotary(torch.zeros((4, 2, 128)), torch.zeros(4, dtype=torch.int32),
+                            torch.zeros(32, dtype=torch.float64), weight=None)
