@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
             normed(m, mate[PAIRS == PAIRS_RELOAD ? v : 0], low ? j + half : j - half, v, false);
             const float2* tv = turn + (low ? jr : jr - half);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = low ? turn_first(x[e], m[e], tv[e]) : turn_second(m[e], x[e], tv[e]);
+            for (int e = 0; e < E; ++e)                // turn_first or turn_second, without a branch
+              x[e] = __fmaf_rn(x[e], tv[e].x, __fmul_rn(m[e], low ? -tv[e].y : tv[e].y));
           }
         }
         *reinterpret_cast<uint4*>(outr + j * ES) = pack_vec<DT>(x);
