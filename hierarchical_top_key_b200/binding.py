@@ -441,9 +441,9 @@ def rotary_inv_freq(rotary_dim: int, *, base: float = 10000.0, scaling: Optional
       "linear"  every pair is slowed by `factor` (positions are interpolated);
       "ntk"     the base grows by factor^(rotary_dim / (rotary_dim - 2)): the fastest pair keeps its speed, the
                 slowest is slowed by `factor`;
-      "ramp"    pairs that turn at least beta_fast times over original_positions keep their speed, those that
-                turn at most beta_slow times are slowed by `factor`, with a ramp linear in the pair's index
-                between; the amplitude is amplitude_factor * ln(factor) + 1."""
+      "ramp"    YaRN (arXiv 2309.00071): pairs that turn at least beta_fast times over original_positions keep
+                their speed, those that turn at most beta_slow times are slowed by `factor`, with a ramp linear in
+                the pair's index between; the amplitude is amplitude_factor * ln(factor) + 1."""
     if rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even and >= 2")
     if not (base > 1 and factor > 0):

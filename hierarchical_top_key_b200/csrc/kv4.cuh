@@ -11,12 +11,14 @@
 //   [256, 288)  a scale code c for each 16 features,
 //               s = (1 + (c & 7) / 8) * 2^((c >> 3) - 20)
 //   [288, 416)  the 64 positional features in bf16, unchanged
-// s is the smallest such value with 7 s >= max|x| of the group, so nothing is
+// s is the smallest such value with 7 s >= max|x| of the group: nothing is
 // clipped and a value is off by at most s / 2 <= max|x| / 12.4 (9/8 is the
-// largest step between scales).  n = x / s to the nearest, ties to even.  n s
-// has 3 + 4 significant bits: bf16 holds it exactly, so what attention
-// multiplies is what reading back returns.  A group beyond 7 * 3840 uses the
-// largest scale and saturates; a NaN counts as 0.
+// largest step between scales) where max|x| lies between 7 * 2^-20, below which
+// the smallest scale stays and a value is off by up to 2^-21, and 7 * 3840 =
+// 26880, beyond which the largest one stays and the group saturates.  n = x / s to
+// the nearest, ties to even.  n s has 3 + 4 significant bits: bf16 holds it
+// exactly, so what attention multiplies is what reading back returns.  A NaN
+// counts as 0.
 #pragma once
 #include "common.cuh"
 

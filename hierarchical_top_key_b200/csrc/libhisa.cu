@@ -368,9 +368,12 @@ hisa_status check_kv4_attn(int32_t batch, int32_t num_queries, int32_t heads, in
   return HISA_OK;
 }
 
-// Parts of each query's keys: as many as give every pair of SMs one work item,
-// at least two 64-key tiles each (one for either SM); and the workspace of one query (its record
-// list and, with parts, their outputs).
+// Parts of each query's keys: the largest number, the same for every query and
+// from top_k alone, with which no pair of SMs has more than one work item, of at
+// least two 64-key tiles each (one for either SM); and the workspace of one query
+// (its record list and, with parts, their outputs).  More than half as many
+// (query, head slice) items as pairs are not split: 38 use 38 of 74 pairs, 75
+// take two rounds, and a launch lasts as long as its longest query.
 struct Kv4Plan {
   int parts, list_ld;
   size_t per_row;

@@ -13,9 +13,10 @@
 //
 // The angle needs more than fp32: at position 10^6 an fp32 product is off by
 // 0.06 rad.  inv_freq / 2 pi is therefore held as a 64-bit fixed-point part of
-// a turn, and position * that (modulo 2^64, an integer multiplication) is the
-// phase exactly; its top 32 bits are the angle in [-1, 1) half turns that
-// sincospi takes.
+// a turn, and position * that (modulo 2^64, an integer multiplication) adds no
+// error but the part's own: one fp64 product, up to |position| * 2^-55 turns for
+// inv_freq up to 1.  The phase's top 32 bits, rounded to fp32 (up to 2^-26
+// turns), are the angle in [-1, 1) half turns that sincospi takes.
 #pragma once
 #include "common.cuh"
 
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) norm_rotary_rows_kernel(con
 //   - weight and bias of a lane's features stay in registers over its rows
 //     where they are few (two vectors a lane), for the occupancy's sake;
 //   - the partner of a half-layout pair lies rot / 2 features away.  With G as
-//     many vectors as that it is the same lane's next or last vector (PAIRED);
+//     many vectors as that it is the same lane's next or last vector (PAIRS_IN_LANE);
 //     otherwise it is loaded again, from L1.  All loads of a row are made
 //     before its first store, so in place is safe.
 
@@ -172,7 +173,11 @@ constexpr int kRotaryTable = 4096;             // (cos, sin) pairs of a block
 
 enum : int { PAIRS_INTERLEAVED, PAIRS_RELOAD, PAIRS_IN_LANE };
 
-// Blocks an SM: enough loads in flight to keep HBM busy.
+// Blocks an SM: enough loads in flight to keep HBM busy.  Chosen on the prompt
+// sizes named above.  At these register caps some bf16 kernels spill (layer norms
+// with PAIRS_RELOAD 24 to 144 bytes, RMS norms with it up to 56, layer norms with
+// PAIRS_IN_LANE 48, rotations in half layout 24; fp32 up to 24); they have not
+// been timed at other caps.
 constexpr int rotary_blocks(int norm, int v) { return v > 5 ? 2 : v > 4 ? 3 : v > 2 ? 4 : norm == NORM_NONE ? 6 : 4; }
 
 template <int DT, int NORM, int V, int PAIRS>
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kRotaryThreads, rotary_blocks(NORM, V)) norm_r
         for (int e = 0; e < E; ++e) sq += NORM == NORM_LAYER ? (x[e] - mean) * (x[e] - mean) : x[e] * x[e];
       }
       for (int o = G >> 1; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-      rs = rsqrtf(sq * inv_n + p.eps);
+      rs = rsqrtf(sq * inv_n + p.eps);                 // off by 2 ulp at most
     }
     // features j .. j + E - 1 of vector `from`, normed (vector v's own, or its partner's)
     auto normed = [&](float (&x)[E], const uint4& from, int j, int v, bool own) {

@@ -418,8 +418,11 @@ HISA_API hisa_status hisa_sparse_attention(const void* q, const void* kv, const 
  * (i, i + rotary_dim / 2).  `reverse` turns by -angle: with the same amplitude
  * the gradient of the rotation, with 1 / amplitude its inverse.  The other
  * features are copied.  Scaled positions (long contexts) are scaled inv_freq
- * and an amplitude.  The angle is exact to 2^-31 turns at every int32
- * position; the products are fp32, rounded once to the dtype.
+ * and an amplitude.  The position is multiplied, without rounding, by the
+ * frequency as a 64-bit fixed-point part of a turn; that part carries the
+ * rounding of one fp64 product, at most |position| * 2^-55 turns for inv_freq
+ * up to 1, and the angle is rounded to fp32, at most 2^-26 turns.  The products
+ * are fp32, rounded once to the dtype.  inv_freq is finite.
  *   x          [tokens, heads, dim] HISA_F32 or HISA_BF16, features
  *              contiguous, the other strides given in elements
  *   positions  [tokens] int32;  inv_freq [rotary_dim / 2] fp64 (radians per
@@ -471,8 +474,10 @@ HISA_API hisa_status hisa_norm_rotary(const void* x, int64_t x_token_stride, int
  *   bytes [288, 416)  the 64 positional features in bf16
  * s is the smallest such value with 7 s >= max|x| of the group (the largest,
  * 3840, if none is: the group saturates) and n = x / s to the nearest, ties to
- * even; a NaN counts as 0.  A feature reads back as n * s, exact in bf16 and at
- * most s / 2 off.
+ * even; a NaN counts as 0.  A feature reads back as n * s, exact in bf16 and, in
+ * a group with max|x| <= 26880, at most s / 2 off: s / 2 is at most
+ * max|x| / 12.4, or 2^-21 where max|x| is below 7 * 2^-20 (the smallest scale).
+ * Larger groups saturate at 26880.
  *   cache  [num_slots, 416] bytes, 32-byte aligned: a cache of pages
  *          [num_pages, page_size] has num_pages * page_size slots, the slot of
  *          row r of page p being p * page_size + r
@@ -505,7 +510,10 @@ HISA_API hisa_status hisa_kv4_read(const void* cache, int64_t num_slots, const i
  * Entries of idx outside [0, L) and repeats are dropped.  A page that is
  * needed and lies outside [0, num_pages) is not dereferenced: the position is
  * dropped and the device status word reports HISA_ERR_INVALID_ARG.
- * num_pages * page_size must fit in int32.
+ * num_pages * page_size must fit in int32.  A logit of -inf weighs nothing (all
+ * of them: as an empty set); one of NaN or +inf makes its head's o and lse NaN.
+ * The softmax weights are rounded to bf16 before the product with the values
+ * (lse and the normaliser come from the unrounded ones).
  * Workspace (16-byte aligned): hisa_workspace_size(HISA_OP_SPARSE_ATTENTION_KV4)
  * bytes, from the shape's batch, num_queries, heads and top_k (the other fields
  * are not read): each query's record list, and where there are few queries (a
