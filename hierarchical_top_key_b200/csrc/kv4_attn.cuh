@@ -49,7 +49,7 @@
 //
 // The weights are rounded to bf16, the type of the values they meet in an MMA (a
 // second half with what the rounding lost would double the output MMAs and what
-// the CTAs send): the output's error against 64 bits is 1.9e-3 to 2.2e-3 of its
+// the CTAs send): the output's error against 64 bits is up to 2.2e-3 of its
 // size, where fp32 weights and one rounding of the output leave 1.7e-3.  The sums
 // are of the unrounded weights, in fp32.  Scaled weights are rounded a second
 // time; only those behind a reference that has moved by 2^64 are scaled.
